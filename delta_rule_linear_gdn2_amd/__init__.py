@@ -9,6 +9,10 @@ Two entry points, both hand-written HIP behind the C ABI in include/gdn2.h:
 * ``gdn2_chunk_bwd``      gradients of the chunkwise forward (gate-aware backward)
 * ``gdn2_mixer_prologue`` / ``gdn2_mixer_epilogue``: the token mixer around the
   recurrence (convolution, SiLU, L2 norm, gate sigmoids; RMS norm and output gate)
+* ``gdn2_mixer_prologue_bwd`` / ``gdn2_mixer_epilogue_bwd``: the mixer's gradients
+* ``gdn2_block_norm_fwd`` / ``gdn2_block_norm_bwd``: the step from one block of a layer
+  to the next (norms, gate, residual scale, dropout) and its gradients
+* ``gdn2_dropout``        counter-based dropout whose mask is never stored
 * ``gdn2_chunk_fwd_gates`` / ``gdn2_recurrent_step_gates``: the same with a gate
   layout (``GATES_*`` flags: scalar erase, write or decay gates, tied write gate)
 
@@ -23,13 +27,21 @@ from .binding import (  # noqa: F401
     GATES_SCALAR_WRITE,
     GATES_TIED,
     Gdn2Error,
+    gdn2_block_norm_bwd,
+    gdn2_block_norm_bwd_workspace_bytes,
+    gdn2_block_norm_fwd,
     gdn2_chunk_bwd,
     gdn2_chunk_bwd_workspace_bytes,
     gdn2_chunk_fwd,
     gdn2_chunk_fwd_gates,
     gdn2_chunk_fwd_workspace_bytes,
+    gdn2_dropout,
     gdn2_mixer_epilogue,
+    gdn2_mixer_epilogue_bwd,
+    gdn2_mixer_epilogue_bwd_workspace_bytes,
     gdn2_mixer_prologue,
+    gdn2_mixer_prologue_bwd,
+    gdn2_mixer_prologue_bwd_workspace_bytes,
     gdn2_recurrent_fwd,
     gdn2_recurrent_step,
     gdn2_recurrent_step_gates,
@@ -46,13 +58,21 @@ __all__ = [
     "GATES_SCALAR_WRITE",
     "GATES_TIED",
     "Gdn2Error",
+    "gdn2_block_norm_bwd",
+    "gdn2_block_norm_bwd_workspace_bytes",
+    "gdn2_block_norm_fwd",
     "gdn2_chunk_bwd",
     "gdn2_chunk_bwd_workspace_bytes",
     "gdn2_chunk_fwd",
     "gdn2_chunk_fwd_gates",
     "gdn2_chunk_fwd_workspace_bytes",
+    "gdn2_dropout",
     "gdn2_mixer_epilogue",
+    "gdn2_mixer_epilogue_bwd",
+    "gdn2_mixer_epilogue_bwd_workspace_bytes",
     "gdn2_mixer_prologue",
+    "gdn2_mixer_prologue_bwd",
+    "gdn2_mixer_prologue_bwd_workspace_bytes",
     "gdn2_recurrent_fwd",
     "gdn2_recurrent_step",
     "gdn2_recurrent_step_gates",

@@ -8,6 +8,7 @@ HIP runtime torch uses, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,10 +25,13 @@ STATUS_NAMES = {
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
 
-EXPORTS = ("gdn2_chunk_bwd", "gdn2_chunk_bwd_noalloc", "gdn2_chunk_bwd_noalloc_max_workspace_bytes",
+EXPORTS = ("gdn2_block_norm_bwd", "gdn2_block_norm_bwd_workspace_bytes", "gdn2_block_norm_fwd",
+           "gdn2_chunk_bwd", "gdn2_chunk_bwd_noalloc", "gdn2_chunk_bwd_noalloc_max_workspace_bytes",
            "gdn2_chunk_bwd_workspace_bytes", "gdn2_chunk_fwd", "gdn2_chunk_fwd_gates",
-           "gdn2_chunk_fwd_workspace_bytes",
-           "gdn2_mixer_epilogue", "gdn2_mixer_prologue", "gdn2_recurrent_fwd", "gdn2_recurrent_step",
+           "gdn2_chunk_fwd_workspace_bytes", "gdn2_dropout",
+           "gdn2_mixer_epilogue", "gdn2_mixer_epilogue_bwd", "gdn2_mixer_epilogue_bwd_workspace_bytes",
+           "gdn2_mixer_prologue", "gdn2_mixer_prologue_bwd", "gdn2_mixer_prologue_bwd_workspace_bytes",
+           "gdn2_recurrent_fwd", "gdn2_recurrent_step",
            "gdn2_recurrent_step_gates", "gdn2_status_string", "gdn2_version")
 
 # gdn2_gate_flags: layout of the gates (b, w, alpha), OR-ed together
@@ -96,6 +100,23 @@ def load(path: str = LIB_PATH):
     lib.gdn2_mixer_prologue.restype = ctypes.c_int
     lib.gdn2_mixer_epilogue.argtypes = [P, P, P, P, ctypes.c_int64, I, F, I, I, P]
     lib.gdn2_mixer_epilogue.restype = ctypes.c_int
+    L, D, U = ctypes.c_int64, ctypes.c_double, ctypes.c_uint64
+    lib.gdn2_block_norm_fwd.argtypes = [P] * 7 + [L, I, F, F, I, I, D, U, U, P, I, I, P]
+    lib.gdn2_block_norm_fwd.restype = ctypes.c_int
+    lib.gdn2_block_norm_bwd.argtypes = [P] * 12 + [L, I, F, F, I, I, D, U, U, P, I, I, P, Z, P]
+    lib.gdn2_block_norm_bwd.restype = ctypes.c_int
+    lib.gdn2_block_norm_bwd_workspace_bytes.argtypes = [L, I]
+    lib.gdn2_block_norm_bwd_workspace_bytes.restype = Z
+    lib.gdn2_dropout.argtypes = [P, P, L, L, D, U, U, P, I, P]
+    lib.gdn2_dropout.restype = ctypes.c_int
+    lib.gdn2_mixer_epilogue_bwd.argtypes = [P] * 7 + [L, I, F, I, I, P, Z, P]
+    lib.gdn2_mixer_epilogue_bwd.restype = ctypes.c_int
+    lib.gdn2_mixer_epilogue_bwd_workspace_bytes.argtypes = [L, I]
+    lib.gdn2_mixer_epilogue_bwd_workspace_bytes.restype = Z
+    lib.gdn2_mixer_prologue_bwd.argtypes = [P] * 25 + [I] * 7 + [F, F, I, P, Z, P]
+    lib.gdn2_mixer_prologue_bwd.restype = ctypes.c_int
+    lib.gdn2_mixer_prologue_bwd_workspace_bytes.argtypes = [I] * 6
+    lib.gdn2_mixer_prologue_bwd_workspace_bytes.restype = Z
     lib.gdn2_status_string.argtypes = [ctypes.c_int]
     lib.gdn2_status_string.restype = ctypes.c_char_p
     lib.gdn2_version.argtypes = []
@@ -488,4 +509,300 @@ def gdn2_mixer_epilogue(o, gate, weight, *, eps=1e-5, act="sigmoid", out=None, s
                                  GATE_ACTS[act], code, _stream(stream))
     if rc != GDN2_OK:
         raise Gdn2Error(rc, "gdn2_mixer_epilogue")
+    return out
+
+
+# --- training operators ------------------------------------------------------
+
+
+def _on_stream(f):
+    """Runs a call on ``stream`` (default: the current stream of its tensors'
+    device), with that device current.  What the call allocates (outputs,
+    workspace) belongs to that stream, so memory another stream is still
+    using is never handed to it, nor its own to another stream too early."""
+
+    @functools.wraps(f)
+    def call(first, *args, stream=None, **kw):
+        import torch
+
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError(f"stream: on {stream.device}, the tensors are on {first.device}")
+            with torch.cuda.stream(stream):
+                return f(first, *args, **kw)
+        if first.is_cuda and first.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return f(first, *args, **kw)
+        return f(first, *args, **kw)
+
+    return call
+
+
+def _run(name, dev, *args):
+    """Calls the C function on the current stream; raises what it refuses."""
+    import torch
+
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a GPU (got {dev})")
+    rc = getattr(load(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != GDN2_OK:
+        raise Gdn2Error(rc, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _buffer(name, t, shape, dtype, dev):
+    """The caller's output tensor, checked, or a new one."""
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check(name, t, shape, dtype, dev)
+    return t
+
+
+def _workspace(t, nbytes, dev):
+    import torch
+
+    if not nbytes:
+        return None, 0
+    if t is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous uint8 on {dev}")
+    elif t.numel() < nbytes:
+        raise ValueError(f"workspace of {t.numel()} bytes < {nbytes}")
+    return t, t.numel()
+
+
+def _rows(name, t):
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name}: needs a last axis of at least one element (shape {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.numel() // t.shape[-1]
+
+
+def _random(seed, offset, offset_device, dev):
+    import torch
+
+    for name, v in (("seed", seed), ("offset", offset)):
+        if not 0 <= v < 1 << 64:
+            raise ValueError(f"{name}: {v} is not in [0, 2^64)")
+    if offset_device is not None:
+        _check("offset_device", offset_device, (1,), torch.int64, dev)
+    return seed, offset, _addr(offset_device)
+
+
+GATE_LAYOUTS = {"none": 0, "channel": 1, "token": 2, "full": 3}
+BLOCK_GATE_ACTS = {"sigmoid": 0, "silu": 1, "identity": 2}
+
+
+def _block_inputs(x, u, gate, gate_layout, gate_act, weight_post, weight_pre):
+    """Checks the inputs that the block norm's two directions share; returns
+    their sizes, types and codes."""
+    import torch
+
+    rows, shape, dev, rdt = _rows("x", x), tuple(x.shape), x.device, x.dtype
+    if u is not None:
+        _check("u", u, shape, u.dtype, dev)
+    if gate_layout not in GATE_LAYOUTS:
+        raise ValueError(f"gate_layout must be one of {tuple(GATE_LAYOUTS)}")
+    if gate_act not in BLOCK_GATE_ACTS:
+        raise ValueError(f"gate_act must be one of {tuple(BLOCK_GATE_ACTS)}")
+    if (gate is None) != (gate_layout == "none"):
+        raise ValueError(f"gate_layout {gate_layout!r} {'needs a' if gate is None else 'takes no'} gate")
+    if gate is not None and u is not None:
+        if gate_layout == "channel":
+            _check("gate", gate, shape[-1:], torch.float32, dev)
+        else:
+            _check("gate", gate, shape if gate_layout == "full" else shape[:-1], u.dtype, dev)
+    for name, w in (("weight_post", weight_post), ("weight_pre", weight_pre)):
+        if w is not None:
+            _check(name, w, shape[-1:], torch.float32, dev)
+    return rows, shape, dev, rdt, GATE_LAYOUTS[gate_layout], BLOCK_GATE_ACTS[gate_act]
+
+
+@_on_stream
+def gdn2_block_norm_fwd(x, u=None, *, gate=None, gate_layout="none", gate_act="sigmoid", weight_post=None,
+                        weight_pre=None, eps=1e-5, residual_scale=1.0, dropout_p=0.0, seed=0, offset=0,
+                        offset_device=None, dtype=None, x_out=None, h=None):
+    """The step from one block to the next: returns ``(x_out, h)``.
+
+        n = u / rms(u) * weight_post                       (u itself without weight_post)
+        x_out = x + residual_scale * dropout(act(gate) * n)
+        h = x_out / rms(x_out) * weight_pre                (None without weight_pre)
+
+    x: the residual stream, [..., D] float32 or bfloat16; u: the block's output,
+    the same shape, or None (then h is the norm of x, and the returned x_out is
+    x).  The stream is u's type, or float32 with bfloat16 blocks.  gate: None, or
+    as gate_layout says: "channel" [D] float32, "token" [...] or "full" [..., D]
+    of u's type; gate_act "sigmoid", "silu" or "identity".  weight_post,
+    weight_pre: [D] float32 or None (no such norm).  dropout_p with seed, offset
+    (integers in [0, 2^64)) and offset_device ([1] int64 on the device, added to
+    offset; or None) as for gdn2_dropout.  dtype: h's type where u is None
+    (default x's).  x_out may be x (in place); x_out and h are allocated when not
+    given.
+    """
+    import torch
+
+    rows, shape, dev, rdt, layout, act = _block_inputs(x, u, gate, gate_layout, gate_act, weight_post, weight_pre)
+    dt = u.dtype if u is not None else dtype or rdt
+    code, rcode = _dtype_code(dt), _dtype_code(rdt)
+    if u is not None:
+        x_out = _buffer("x_out", x_out, shape, rdt, dev)
+    elif x_out is not None:
+        raise ValueError("x_out: there is none without u")
+    if weight_pre is not None:
+        h = _buffer("h", h, shape, dt, dev)
+    elif h is not None:
+        raise ValueError("h: there is none without weight_pre")
+    _run("gdn2_block_norm_fwd", dev, x.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
+         _addr(x_out), _addr(h), rows, shape[-1], eps, residual_scale, layout, act, dropout_p,
+         *_random(seed, offset, offset_device, dev), code, rcode)
+    return (x if u is None else x_out), h
+
+
+def gdn2_block_norm_bwd_workspace_bytes(rows, D) -> int:
+    return int(load().gdn2_block_norm_bwd_workspace_bytes(rows, D))
+
+
+@_on_stream
+def gdn2_block_norm_bwd(x_out, u, d_x_out, d_h, *, gate=None, gate_layout="none", gate_act="sigmoid", weight_post=None,
+                        weight_pre=None, eps=1e-5, residual_scale=1.0, dropout_p=0.0, seed=0, offset=0,
+                        offset_device=None, d_x=None, d_u=None, d_gate=None, want_d_gate=True, want_d_weights=True,
+                        workspace=None):
+    """Gradients of gdn2_block_norm_fwd for the loss <d_x_out, x_out> + <d_h, h>.
+
+    x_out: the stream the forward call returned; u and the keyword arguments:
+    the forward call's; d_x_out: like x_out, or None for zero; d_h: like h, None
+    exactly when weight_pre is.  Returns dict(d_x, d_u, d_gate, d_weight_post,
+    d_weight_pre), None in the place of what has no input or is not wanted.  d_x
+    may be d_x_out (in place).  ``workspace`` (uint8) is allocated when not given.
+    """
+    import torch
+
+    rows, shape, dev, rdt, layout, act = _block_inputs(x_out, u, gate, gate_layout, gate_act, weight_post, weight_pre)
+    D = shape[-1]
+    dt = u.dtype if u is not None else d_h.dtype if d_h is not None else rdt
+    code, rcode = _dtype_code(dt), _dtype_code(rdt)
+    if d_x_out is not None:
+        _check("d_x_out", d_x_out, shape, rdt, dev)
+    if (d_h is None) != (weight_pre is None):
+        raise ValueError("d_h and weight_pre: both or neither")
+    if d_h is not None:
+        _check("d_h", d_h, shape, dt, dev)
+    d_x = _buffer("d_x", d_x, shape, rdt, dev)
+    if u is not None:
+        d_u = _buffer("d_u", d_u, shape, dt, dev)
+    if gate is not None and want_d_gate:
+        d_gate = _buffer("d_gate", d_gate, tuple(gate.shape), gate.dtype, dev)
+    want = want_d_weights
+    d_post = torch.empty(D, dtype=torch.float32, device=dev) if want and weight_post is not None else None
+    d_pre = torch.empty(D, dtype=torch.float32, device=dev) if want and weight_pre is not None else None
+    sums = d_post is not None or d_pre is not None or (d_gate is not None and gate_layout == "channel")
+    workspace, ws_bytes = _workspace(workspace, gdn2_block_norm_bwd_workspace_bytes(rows, D) if sums else 0, dev)
+    _run("gdn2_block_norm_bwd", dev, x_out.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
+         _addr(d_x_out), _addr(d_h), d_x.data_ptr(), _addr(d_u), _addr(d_gate), _addr(d_post), _addr(d_pre), rows, D,
+         eps, residual_scale, layout, act, dropout_p, *_random(seed, offset, offset_device, dev), code, rcode,
+         _addr(workspace), ws_bytes)
+    return {"d_x": d_x, "d_u": d_u, "d_gate": d_gate, "d_weight_post": d_post, "d_weight_pre": d_pre}
+
+
+@_on_stream
+def gdn2_dropout(x, p, seed, offset=0, *, offset_device=None, out=None):
+    """Counter-based dropout of x ([..., D] float32 or bfloat16): the mask comes
+    from (seed, offset) and each element's position and is never stored; the
+    gradient is the same call on the gradient.  p is rounded to a multiple of
+    2^-16; kept elements are divided by 1 - p.  offset_device: [1] int64 on the
+    device, added to offset when the kernel runs (replayed graphs), or None.
+    ``out`` may be x (in place)."""
+    rows, dev = _rows("x", x), x.device
+    code = _dtype_code(x.dtype)
+    out = _buffer("out", out, tuple(x.shape), x.dtype, dev)
+    _run("gdn2_dropout", dev, x.data_ptr(), out.data_ptr(), rows, x.shape[-1], p,
+         *_random(seed, offset, offset_device, dev), code)
+    return out
+
+
+def gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv) -> int:
+    return int(load().gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv))
+
+
+@_on_stream
+def gdn2_mixer_epilogue_bwd(o, gate, weight, d_y, *, eps=1e-5, act="sigmoid", want_d_weight=True, workspace=None):
+    """Gradients of gdn2_mixer_epilogue for the loss <d_y, y>: dict(d_o, d_gate,
+    d_weight), d_weight None when not wanted.  ``workspace`` (uint8) is
+    allocated when not given."""
+    import torch
+
+    rows, dv, shape, dev, dt = _rows("o", o), o.shape[-1], tuple(o.shape), o.device, o.dtype
+    code = _dtype_code(dt)
+    _check("gate", gate, shape, dt, dev)
+    _check("weight", weight, (dv,), torch.float32, dev)
+    _check("d_y", d_y, shape, dt, dev)
+    if act not in GATE_ACTS:
+        raise ValueError(f"act must be one of {tuple(GATE_ACTS)}")
+    d_o, d_gate = torch.empty_like(o), torch.empty_like(o)
+    d_weight = torch.empty_like(weight) if want_d_weight else None
+    workspace, ws_bytes = _workspace(workspace, gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv) if want_d_weight else 0,
+                                     dev)
+    _run("gdn2_mixer_epilogue_bwd", dev, o.data_ptr(), gate.data_ptr(), weight.data_ptr(), d_y.data_ptr(),
+         d_o.data_ptr(), d_gate.data_ptr(), _addr(d_weight), rows, dv, eps, GATE_ACTS[act], code, _addr(workspace),
+         ws_bytes)
+    return {"d_o": d_o, "d_gate": d_gate, "d_weight": d_weight}
+
+
+def gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, kernel_size) -> int:
+    return int(load().gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, kernel_size))
+
+
+@_on_stream
+def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit, d_q, d_k, d_v, d_b, d_w, *,
+                            conv_state=None, d_conv_state_out=None, output_d_conv_state=False, cu_seqlens=None,
+                            q_scale=1.0, eps_l2=1e-6, want_d_conv=True, workspace=None):
+    """Gradients of gdn2_mixer_prologue for the loss <d_q, q> + <d_k, k> + <d_v, v>
+    + <d_b, b> + <d_w, w> + <d_conv_state_out, final convolution state>.
+
+    The inputs are the forward call's (conv_state: its initial state or None);
+    d_q, d_k, d_b: [B, T, H, dk] and d_v, d_w: [B, T, H, dv] of the inputs' type;
+    d_conv_state_out: [N, H * (2 dk + dv), K - 1] float32 or None.  Returns
+    dict(d_xq, d_xk, d_xv, d_conv_q, d_conv_k, d_conv_v, d_b_logit, d_w_logit,
+    d_conv_state), None in the place of what is not wanted.  ``workspace``
+    (uint8) is allocated when not given.
+    """
+    import torch
+
+    B, T, H, dk = xq.shape
+    dv = xv.shape[-1]
+    K = conv_q.shape[-1]
+    dev, dt = xq.device, xq.dtype
+    code = _dtype_code(dt)
+    N = B if cu_seqlens is None else int(cu_seqlens.shape[0]) - 1
+    for name, t, width in (("xq", xq, dk), ("xk", xk, dk), ("b_logit", b_logit, dk), ("xv", xv, dv),
+                           ("w_logit", w_logit, dv), ("d_q", d_q, dk), ("d_k", d_k, dk), ("d_b", d_b, dk),
+                           ("d_v", d_v, dv), ("d_w", d_w, dv)):
+        _check(name, t, (B, T, H, width), dt, dev)
+    for name, t, width in (("conv_q", conv_q, dk), ("conv_k", conv_k, dk), ("conv_v", conv_v, dv)):
+        _check(name, t, (H * width, K), torch.float32, dev)
+    st_shape = (N, H * (2 * dk + dv), K - 1)
+    for name, t in (("conv_state", conv_state), ("d_conv_state_out", d_conv_state_out)):
+        if t is not None:
+            _check(name, t, st_shape, torch.float32, dev)
+    if cu_seqlens is not None:
+        _check("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+    out = {"d_xq": torch.empty_like(xq), "d_xk": torch.empty_like(xk), "d_xv": torch.empty_like(xv)}
+    for name, w in (("d_conv_q", conv_q), ("d_conv_k", conv_k), ("d_conv_v", conv_v)):
+        out[name] = torch.empty_like(w) if want_d_conv else None
+    out["d_b_logit"], out["d_w_logit"] = torch.empty_like(b_logit), torch.empty_like(w_logit)
+    out["d_conv_state"] = torch.empty(st_shape, dtype=torch.float32, device=dev) if output_d_conv_state else None
+    need = gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, K) if want_d_conv else 0
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    _run("gdn2_mixer_prologue_bwd", dev, xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), conv_q.data_ptr(),
+         conv_k.data_ptr(), conv_v.data_ptr(), b_logit.data_ptr(), w_logit.data_ptr(), _addr(conv_state),
+         d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), d_b.data_ptr(), d_w.data_ptr(), _addr(d_conv_state_out),
+         *(_addr(t) for t in out.values()), _addr(cu_seqlens), B, T, H, dk, dv, K, N, q_scale, eps_l2, code,
+         _addr(workspace), ws_bytes)
     return out

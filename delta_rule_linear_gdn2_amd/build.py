@@ -26,6 +26,9 @@ SOURCES = [
     "chunk_bwd.hip",
     "chunk_bwd_mfma.hip",
     "mixer.hip",
+    "mixer_bwd.hip",
+    "block.hip",
+    "colsum.hip",
     "scratch.hip",
     "segments.hip",
 ]

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "gdn2.h"
 #include "launch.hpp"
@@ -331,6 +332,271 @@ gdn2_status mixer_epilogue(const void* o, const void* gate, const float* weight,
     return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
 }
 
+// Spans of a call's inputs and outputs: every output must be clear of every
+// input and of the other outputs, but that output may_out may be input may_in
+// exactly (in place).
+gdn2_status check_spans(std::initializer_list<Span> in, std::initializer_list<Span> out, int may_out = -1,
+                        int may_in = -1)
+{
+    int i = 0;
+    for (const Span& o : out) {
+        int j = 0;
+        for (const Span& x : in) {
+            const bool in_place = i == may_out && j == may_in && o.lo == x.lo;
+            if (!in_place && overlap(o, x)) return GDN2_ERR_ALIAS;
+            ++j;
+        }
+        j = 0;
+        for (const Span& p : out)
+            if (j++ < i && overlap(o, p)) return GDN2_ERR_ALIAS;
+        ++i;
+    }
+    return GDN2_OK;
+}
+
+bool misaligned(std::initializer_list<const void*> ptrs)
+{
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return true;
+    return false;
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 40;  // byte counts of [rows, D] stay far inside 64 bits
+
+// The dropout arguments, checked: p is a probability, the device offset aligned.
+gdn2_status dropout_args(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_device,
+                         gdn2::DropoutArgs& d)
+{
+    if (!(p >= 0.0 && p <= 1.0)) return GDN2_ERR_BAD_SHAPE;
+    if (reinterpret_cast<uintptr_t>(offset_device) & 7u) return GDN2_ERR_MISALIGNED;
+    const uint32_t threshold = uint32_t(p * 65536.0 + 0.5);
+    d = {threshold, threshold < 65536 ? float(65536.0 / (65536 - threshold)) : 0.f, seed, offset, offset_device};
+    return GDN2_OK;
+}
+
+// Type, size, gate and dropout checks that the block norm's two directions share.
+gdn2_status block_norm_check(bool has_u, const void* gate, const float* weight_post, int64_t rows, int32_t D,
+                             float eps, int32_t gate_layout, int32_t gate_act, double p, uint64_t seed,
+                             uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype, gdn2_dtype rdtype,
+                             gdn2::DropoutArgs& drop)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    if (rdtype != GDN2_DTYPE_F32 && rdtype != dtype) return GDN2_ERR_BAD_DTYPE;
+    if (rows < 0 || rows > kMaxRows || D <= 0 || !(eps > 0.f)) return GDN2_ERR_BAD_SHAPE;
+    if (gate_layout < 0 || gate_layout > 3 || gate_act < 0 || gate_act > 2) return GDN2_ERR_BAD_SHAPE;
+    if (D > gdn2::kBlockMaxD) return GDN2_ERR_UNSUPPORTED;
+    if (gdn2_status s = dropout_args(p, seed, offset, offset_device, drop)) return s;
+    if (gate_layout == gdn2::kGateNone && gate) return GDN2_ERR_BAD_SHAPE;
+    if (rows > 0 && !has_u && (gate_layout != gdn2::kGateNone || weight_post || drop.threshold))
+        return GDN2_ERR_BAD_SHAPE;
+    if (gate_layout != gdn2::kGateNone && rows > 0 && !gate) return GDN2_ERR_NULL_POINTER;
+    return GDN2_OK;
+}
+
+int64_t gate_bytes(int32_t layout, int64_t rows, int32_t D, int eb)
+{
+    return layout == gdn2::kGateChannel ? int64_t(D) * 4
+           : layout == gdn2::kGateToken ? rows * eb
+           : layout == gdn2::kGateFull  ? rows * D * eb
+                                        : 0;
+}
+
+Span span_or_none(const void* p, int64_t bytes) { return span(p, p ? bytes : 0); }
+
+gdn2_status block_norm_fwd(const void* x, const void* u, const void* gate, const float* weight_post,
+                           const float* weight_pre, void* x_out, void* h, int64_t rows, int32_t D, float eps,
+                           float scale, int32_t gate_layout, int32_t gate_act, double p, uint64_t seed,
+                           uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype, gdn2_dtype rdtype,
+                           void* stream)
+{
+    gdn2::DropoutArgs drop;
+    if (gdn2_status s = block_norm_check(u != nullptr, gate, weight_post, rows, D, eps, gate_layout, gate_act, p, seed,
+                                         offset, offset_device, dtype, rdtype, drop))
+        return s;
+    if (!u && x_out) return GDN2_ERR_BAD_SHAPE;
+    if (rows > 0 && (!x || (u && !x_out) || (!u && !h) || !weight_pre != !h)) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({x, u, gate, weight_post, weight_pre, x_out, h})) return GDN2_ERR_MISALIGNED;
+    const int eb = element_bytes(dtype), rb = element_bytes(rdtype);
+    const int64_t n = rows * D, wb = int64_t(D) * 4;
+    if (gdn2_status s = check_spans(
+            {span_or_none(x, n * rb), span_or_none(u, n * eb), span_or_none(gate, gate_bytes(gate_layout, rows, D, eb)),
+             span_or_none(weight_post, wb), span_or_none(weight_pre, wb), span_or_none(offset_device, 8)},
+            {span_or_none(x_out, n * rb), span_or_none(h, n * eb)}, 0, 0))
+        return s;
+    gdn2::BlockNormArgs a{x,    u, gate, weight_post, weight_pre, x_out,    h,   rows,
+                          D, eps, scale, gate_layout, gate_act,   drop};
+    const hipError_t e = gdn2::launch_block_norm_fwd(a, dtype == GDN2_DTYPE_BF16, rdtype == GDN2_DTYPE_BF16,
+                                                     static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+size_t block_norm_bwd_workspace(int64_t rows, int32_t D)
+{
+    if (rows <= 0 || rows > kMaxRows || D <= 0 || D > gdn2::kBlockMaxD) return 0;
+    return align256(size_t(gdn2::block_bwd_partials(rows, D)) * 3 * size_t(D) * 4);
+}
+
+gdn2_status block_norm_bwd(const void* x_out, const void* u, const void* gate, const float* weight_post,
+                           const float* weight_pre, const void* d_x_out, const void* d_h, void* d_x, void* d_u,
+                           void* d_gate, float* d_weight_post, float* d_weight_pre, int64_t rows, int32_t D, float eps,
+                           float scale, int32_t gate_layout, int32_t gate_act, double p, uint64_t seed,
+                           uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype, gdn2_dtype rdtype,
+                           void* workspace, size_t workspace_bytes, void* stream)
+{
+    gdn2::DropoutArgs drop;
+    if (gdn2_status s = block_norm_check(u != nullptr, gate, weight_post, rows, D, eps, gate_layout, gate_act, p, seed,
+                                         offset, offset_device, dtype, rdtype, drop))
+        return s;
+    if ((!u && d_u) || (gate_layout == gdn2::kGateNone && d_gate) || (!weight_post && d_weight_post) ||
+        (!weight_pre && d_weight_pre))
+        return GDN2_ERR_BAD_SHAPE;
+    if (rows > 0 && (!d_x || (u && !d_u) || (weight_pre && !x_out) || (!d_x_out && !d_h) || !weight_pre != !d_h))
+        return GDN2_ERR_NULL_POINTER;
+    if (misaligned({x_out, u, gate, weight_post, weight_pre, d_x_out, d_h, d_x, d_u, d_gate, d_weight_post,
+                    d_weight_pre, workspace}))
+        return GDN2_ERR_MISALIGNED;
+    const bool sums = d_weight_post || d_weight_pre || (gate_layout == gdn2::kGateChannel && d_gate);
+    const size_t need = sums ? block_norm_bwd_workspace(rows, D) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN2_ERR_WORKSPACE;
+    const int eb = element_bytes(dtype), rb = element_bytes(rdtype);
+    const int64_t n = rows * D, wb = int64_t(D) * 4, gb = gate_bytes(gate_layout, rows, D, eb);
+    if (gdn2_status s = check_spans(
+            {span_or_none(d_x_out, n * rb), span_or_none(weight_pre ? x_out : nullptr, n * rb), span_or_none(u, n * eb),
+             span_or_none(gate, gb), span_or_none(weight_post, wb), span_or_none(weight_pre, wb),
+             span_or_none(d_h, n * eb), span_or_none(offset_device, 8)},
+            {span_or_none(d_x, n * rb), span_or_none(d_u, n * eb), span_or_none(d_gate, gb),
+             span_or_none(d_weight_post, wb), span_or_none(d_weight_pre, wb),
+             span_or_none(need ? workspace : nullptr, int64_t(need))},
+            0, 0))
+        return s;
+    gdn2::BlockNormBwdArgs a{x_out, u,     gate,         weight_post,  weight_pre, d_x_out, d_h,   d_x,         d_u,
+                             d_gate, d_weight_post, d_weight_pre, rows, D,       eps,   scale,       gate_layout,
+                             gate_act, drop, static_cast<float*>(workspace)};
+    const hipError_t e = gdn2::launch_block_norm_bwd(a, dtype == GDN2_DTYPE_BF16, rdtype == GDN2_DTYPE_BF16,
+                                                     static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+gdn2_status dropout(const void* x, void* y, int64_t rows, int64_t D, double p, uint64_t seed, uint64_t offset,
+                    const uint64_t* offset_device, gdn2_dtype dtype, void* stream)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    constexpr int64_t kMost = int64_t(1) << 56;
+    if (rows < 0 || D <= 0 || D > kMost || (rows > 0 && (D - 1) / 8 + 1 > (kMost - 1) / rows)) return GDN2_ERR_BAD_SHAPE;
+    gdn2::DropoutArgs drop;
+    if (gdn2_status s = dropout_args(p, seed, offset, offset_device, drop)) return s;
+    if (rows > 0 && (!x || !y)) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({x, y})) return GDN2_ERR_MISALIGNED;
+    const int eb = element_bytes(dtype);
+    if (gdn2_status s = check_spans({span_or_none(x, rows * D * eb), span_or_none(offset_device, 8)},
+                                    {span_or_none(y, rows * D * eb)}, 0, 0))
+        return s;
+    const hipError_t e = gdn2::launch_dropout({x, y, rows, D, drop}, dtype == GDN2_DTYPE_BF16,
+                                              static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+size_t epilogue_bwd_workspace(int64_t rows, int32_t dv)
+{
+    if (rows <= 0 || rows > kMaxRows || !supported_head(dv)) return 0;
+    return align256(size_t(gdn2::epilogue_bwd_partials(rows, dv)) * size_t(dv) * 4);
+}
+
+gdn2_status mixer_epilogue_bwd(const void* o, const void* gate, const float* weight, const void* d_y, void* d_o,
+                               void* d_gate, float* d_weight, int64_t rows, int32_t dv, float eps, int32_t act,
+                               gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    if (rows < 0 || rows > kMaxRows || dv <= 0 || (act != 0 && act != 1) || !(eps > 0.f)) return GDN2_ERR_BAD_SHAPE;
+    if (!supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
+    if (rows > 0 && (!o || !gate || !weight || !d_y || !d_o || !d_gate)) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({o, gate, weight, d_y, d_o, d_gate, d_weight, workspace})) return GDN2_ERR_MISALIGNED;
+    const size_t need = d_weight ? epilogue_bwd_workspace(rows, dv) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN2_ERR_WORKSPACE;
+    const int64_t n = rows * dv * element_bytes(dtype), wb = int64_t(dv) * 4;
+    if (gdn2_status s = check_spans({span_or_none(o, n), span_or_none(gate, n), span_or_none(weight, wb), span_or_none(d_y, n)},
+                                    {span_or_none(d_o, n), span_or_none(d_gate, n), span_or_none(d_weight, wb),
+                                     span_or_none(need ? workspace : nullptr, int64_t(need))}))
+        return s;
+    gdn2::EpilogueBwdArgs a{o, gate, weight, d_y, d_o, d_gate, d_weight, rows, dv, eps, act, static_cast<float*>(workspace)};
+    const hipError_t e = gdn2::launch_mixer_epilogue_bwd(a, dtype == GDN2_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+size_t prologue_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t K)
+{
+    if (B <= 0 || T <= 0 || H <= 0 || !supported_head(dk) || !supported_head(dv) || K < 1 || K > 16) return 0;
+    const int64_t run = gdn2::prologue_bwd_run(B, T, H, dk, dv, K), runs = (int64_t(T) + run - 1) / run;
+    return align256(size_t(B) * size_t(runs) * size_t(H) * size_t(2 * dk + dv) * size_t(K) * 4);
+}
+
+gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&conv)[3], const void* const (&logit)[2],
+                               const float* conv_state_in, const void* const (&d_out)[3],
+                               const void* const (&d_gate)[2], const float* d_state_out, void* const (&d_x)[3],
+                               float* const (&d_conv)[3], void* const (&d_logit)[2], float* d_state_in,
+                               const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
+                               int32_t K, int32_t num_seqs, float q_scale, float eps_l2, gdn2_dtype dtype,
+                               void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    if (B <= 0 || T < 0 || H <= 0 || dk <= 0 || dv <= 0 || K < 1 || K > 16) return GDN2_ERR_BAD_SHAPE;
+    if (cu_seqlens && (B != 1 || num_seqs <= 0)) return GDN2_ERR_BAD_SHAPE;
+    if (!(eps_l2 >= 0.f)) return GDN2_ERR_BAD_SHAPE;
+    if (!supported_head(dk) || !supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
+    const int32_t N = cu_seqlens ? num_seqs : B;
+    if (T > 0)
+        for (const void* p : {x[0], x[1], x[2], static_cast<const void*>(conv[0]), static_cast<const void*>(conv[1]),
+                              static_cast<const void*>(conv[2]), logit[0], logit[1], d_out[0], d_out[1], d_out[2],
+                              d_gate[0], d_gate[1], static_cast<const void*>(d_x[0]), static_cast<const void*>(d_x[1]),
+                              static_cast<const void*>(d_x[2]), static_cast<const void*>(d_logit[0]),
+                              static_cast<const void*>(d_logit[1])})
+            if (!p) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({x[0], x[1], x[2], conv[0], conv[1], conv[2], logit[0], logit[1], conv_state_in, d_out[0], d_out[1],
+                    d_out[2], d_gate[0], d_gate[1], d_state_out, d_x[0], d_x[1], d_x[2], d_conv[0], d_conv[1],
+                    d_conv[2], d_logit[0], d_logit[1], d_state_in, workspace}))
+        return GDN2_ERR_MISALIGNED;
+    if (cu_seqlens && (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)) return GDN2_ERR_MISALIGNED;
+    const size_t need = d_conv[0] || d_conv[1] || d_conv[2] ? prologue_bwd_workspace(B, T, H, dk, dv, K) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN2_ERR_WORKSPACE;
+    const int64_t tokens = int64_t(B) * T * H, nk = tokens * dk * element_bytes(dtype),
+                  nv = tokens * dv * element_bytes(dtype), ck = int64_t(H) * dk * K * 4, cv = int64_t(H) * dv * K * 4;
+    const int64_t st = int64_t(N) * H * (2 * dk + dv) * (K - 1) * 4;
+    if (gdn2_status s = check_spans(
+            {span_or_none(x[0], nk), span_or_none(x[1], nk), span_or_none(x[2], nv), span_or_none(conv[0], ck),
+             span_or_none(conv[1], ck), span_or_none(conv[2], cv), span_or_none(logit[0], nk),
+             span_or_none(logit[1], nv), span_or_none(conv_state_in, st), span_or_none(d_out[0], nk),
+             span_or_none(d_out[1], nk), span_or_none(d_out[2], nv), span_or_none(d_gate[0], nk),
+             span_or_none(d_gate[1], nv), span_or_none(d_state_out, st), span_or_none(cu_seqlens, int64_t(N + 1) * 4)},
+            {span_or_none(d_x[0], nk), span_or_none(d_x[1], nk), span_or_none(d_x[2], nv), span_or_none(d_conv[0], ck),
+             span_or_none(d_conv[1], ck), span_or_none(d_conv[2], cv), span_or_none(d_logit[0], nk),
+             span_or_none(d_logit[1], nv), span_or_none(d_state_in, st),
+             span_or_none(need ? workspace : nullptr, int64_t(need))}))
+        return s;
+    gdn2::PrologueBwdArgs a{};
+    for (int i = 0; i < 3; ++i) {
+        a.x[i] = x[i];
+        a.conv[i] = conv[i];
+        a.d_out[i] = d_out[i];
+        a.d_x[i] = d_x[i];
+        a.d_conv[i] = d_conv[i];
+    }
+    for (int i = 0; i < 2; ++i) {
+        a.logit[i] = logit[i];
+        a.d_gate[i] = d_gate[i];
+        a.d_logit[i] = d_logit[i];
+    }
+    a.conv_state_in = conv_state_in;
+    a.d_state_out = d_state_out;
+    a.d_state_in = d_state_in;
+    a.cu_seqlens = cu_seqlens;
+    a.B = B, a.T = T, a.H = H, a.dk = dk, a.dv = dv, a.K = K, a.N = N;
+    a.q_scale = q_scale, a.eps_l2 = eps_l2;
+    a.run = gdn2::prologue_bwd_run(B, T, H, dk, dv, K);
+    a.partial = need ? static_cast<float*>(workspace) : nullptr;
+    const hipError_t e = gdn2::launch_mixer_prologue_bwd(a, dtype == GDN2_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
 // Workspace regions of the backward pass.  FP32 path: chunk-start states,
 // chunk-end state gradients (slots x H x dk x dv FP32 each, per batch row), U
 // and dX rows (B x T x H x dv FP32 each) and each chunk's prepared triangular
@@ -588,6 +854,71 @@ gdn2_status gdn2_mixer_epilogue(const void* o, const void* gate, const float* we
                                 int32_t dv, float eps, int32_t gate_act, gdn2_dtype dtype, void* stream)
 {
     return mixer_epilogue(o, gate, weight, y, rows, dv, eps, gate_act, dtype, stream);
+}
+
+gdn2_status gdn2_block_norm_fwd(const void* x, const void* u, const void* gate, const float* weight_post,
+                                const float* weight_pre, void* x_out, void* h, int64_t rows, int32_t D, float eps,
+                                float residual_scale, int32_t gate_layout, int32_t gate_act, double dropout_p,
+                                uint64_t seed, uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype,
+                                gdn2_dtype residual_dtype, void* stream)
+{
+    return block_norm_fwd(x, u, gate, weight_post, weight_pre, x_out, h, rows, D, eps, residual_scale, gate_layout,
+                          gate_act, dropout_p, seed, offset, offset_device, dtype, residual_dtype, stream);
+}
+
+gdn2_status gdn2_block_norm_bwd(const void* x_out, const void* u, const void* gate, const float* weight_post,
+                                const float* weight_pre, const void* d_x_out, const void* d_h, void* d_x, void* d_u,
+                                void* d_gate, float* d_weight_post, float* d_weight_pre, int64_t rows, int32_t D,
+                                float eps, float residual_scale, int32_t gate_layout, int32_t gate_act,
+                                double dropout_p, uint64_t seed, uint64_t offset, const uint64_t* offset_device,
+                                gdn2_dtype dtype, gdn2_dtype residual_dtype, void* workspace, size_t workspace_bytes,
+                                void* stream)
+{
+    return block_norm_bwd(x_out, u, gate, weight_post, weight_pre, d_x_out, d_h, d_x, d_u, d_gate, d_weight_post,
+                          d_weight_pre, rows, D, eps, residual_scale, gate_layout, gate_act, dropout_p, seed, offset,
+                          offset_device, dtype, residual_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t gdn2_block_norm_bwd_workspace_bytes(int64_t rows, int32_t D) { return block_norm_bwd_workspace(rows, D); }
+
+gdn2_status gdn2_dropout(const void* x, void* y, int64_t rows, int64_t D, double dropout_p, uint64_t seed,
+                         uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype, void* stream)
+{
+    return dropout(x, y, rows, D, dropout_p, seed, offset, offset_device, dtype, stream);
+}
+
+gdn2_status gdn2_mixer_epilogue_bwd(const void* o, const void* gate, const float* weight, const void* d_y, void* d_o,
+                                    void* d_gate, float* d_weight, int64_t rows, int32_t dv, float eps,
+                                    int32_t gate_act, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream)
+{
+    return mixer_epilogue_bwd(o, gate, weight, d_y, d_o, d_gate, d_weight, rows, dv, eps, gate_act, dtype, workspace,
+                              workspace_bytes, stream);
+}
+
+size_t gdn2_mixer_epilogue_bwd_workspace_bytes(int64_t rows, int32_t dv) { return epilogue_bwd_workspace(rows, dv); }
+
+gdn2_status gdn2_mixer_prologue_bwd(const void* xq, const void* xk, const void* xv, const float* conv_q,
+                                    const float* conv_k, const float* conv_v, const void* b_logit,
+                                    const void* w_logit, const float* conv_state_in, const void* d_q, const void* d_k,
+                                    const void* d_v, const void* d_b, const void* d_w, const float* d_conv_state_out,
+                                    void* d_xq, void* d_xk, void* d_xv, float* d_conv_q, float* d_conv_k,
+                                    float* d_conv_v, void* d_b_logit, void* d_w_logit, float* d_conv_state_in,
+                                    const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t dk,
+                                    int32_t dv, int32_t kernel_size, int32_t num_seqs, float q_scale, float eps_l2,
+                                    gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return mixer_prologue_bwd({xq, xk, xv}, {conv_q, conv_k, conv_v}, {b_logit, w_logit}, conv_state_in,
+                              {d_q, d_k, d_v}, {d_b, d_w}, d_conv_state_out, {d_xq, d_xk, d_xv},
+                              {d_conv_q, d_conv_k, d_conv_v}, {d_b_logit, d_w_logit}, d_conv_state_in, cu_seqlens, B,
+                              T, H, dk, dv, kernel_size, num_seqs, q_scale, eps_l2, dtype, workspace, workspace_bytes,
+                              stream);
+}
+
+size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
+                                               int32_t kernel_size)
+{
+    return prologue_bwd_workspace(B, T, H, dk, dv, kernel_size);
 }
 
 }  // extern "C"

@@ -139,7 +139,120 @@ struct EpilogueArgs {
     int32_t act;  // 0 sigmoid, 1 SiLU
 };
 
+// Dropout: element e of a row is kept when its 16 random bits are at least the
+// threshold, and then multiplied by `keep` = 2^16 / (2^16 - threshold) (0 when
+// nothing is kept).  threshold 0: no dropout, no bits are made.
+struct DropoutArgs {
+    uint32_t threshold;
+    float keep;
+    uint64_t seed, offset;
+    const uint64_t* offset_device;  // added to offset; or null
+};
+
+struct DropoutCall {
+    const void* x;
+    void* y;
+    int64_t rows, D;
+    DropoutArgs drop;
+};
+
+// The step from one block to the next: x_out = x + scale * dropout(act(gate) *
+// norm(u)), h = norm(x_out).  Null: u (h is the norm of x), w_post (no norm of
+// u), w_pre with h (no norm of x_out).
+constexpr int32_t kBlockMaxD = 16384;
+constexpr int32_t kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3;
+struct BlockNormArgs {
+    const void* x;
+    const void* u;
+    const void* gate;
+    const float* w_post;
+    const float* w_pre;
+    void* x_out;
+    void* h;
+    int64_t rows;
+    int32_t D;
+    float eps, scale;
+    int32_t gate_layout, act;  // act: 0 sigmoid, 1 SiLU, 2 identity
+    DropoutArgs drop;
+};
+
+// Its gradients.  Null: d_x_out (zero), w_pre with d_h, u with d_u, w_post,
+// and any of d_gate, d_w_post, d_w_pre (not wanted).
+struct BlockNormBwdArgs {
+    const void* x;  // the stored stream, x_out of the forward call
+    const void* u;
+    const void* gate;
+    const float* w_post;
+    const float* w_pre;
+    const void* d_x_out;
+    const void* d_h;
+    void* d_x;
+    void* d_u;
+    void* d_gate;
+    float* d_w_post;
+    float* d_w_pre;
+    int64_t rows;
+    int32_t D;
+    float eps, scale;
+    int32_t gate_layout, act;
+    DropoutArgs drop;
+    float* partial;  // [block_bwd_partials(rows, D)][sums * D], the wanted sums in the order post, pre, channel gate
+};
+int64_t block_bwd_partials(int64_t rows, int32_t D);
+
+struct EpilogueBwdArgs {
+    const void* o;
+    const void* gate;
+    const float* weight;
+    const void* d_y;
+    void* d_o;
+    void* d_gate;
+    float* d_weight;  // or null
+    int64_t rows;
+    int32_t dv;
+    float eps;
+    int32_t act;
+    float* partial;  // [epilogue_bwd_partials(rows, dv)][dv]
+};
+int64_t epilogue_bwd_partials(int64_t rows, int32_t dv);
+
+struct PrologueBwdArgs {
+    const void* x[3];         // xq, xk, xv
+    const float* conv[3];     // [H * d][K]
+    const void* logit[2];     // b, w
+    const float* conv_state_in;
+    const void* d_out[3];     // dq, dk, dv
+    const void* d_gate[2];    // db, dw
+    const float* d_state_out;
+    void* d_x[3];
+    float* d_conv[3];         // or null
+    void* d_logit[2];
+    float* d_state_in;        // or null
+    const int32_t* cu_seqlens;
+    int32_t B, T, H, dk, dv, K, N;
+    float q_scale, eps_l2;
+    int32_t run;              // tokens per wavefront
+    float* partial;           // [B * ceil(T / run)][H * (2 dk + dv) * K], or null when no filter gradient is wanted
+};
+// Tokens per wavefront of the prologue's backward for these sizes.
+int32_t prologue_bwd_run(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t K);
+
+// out[i][c - begin] = sum over the P rows of partial[.][c], for the columns
+// [begin, end[i]) of segment i (begin: the end of segment i - 1).
+struct ColumnSumArgs {
+    const float* partial;
+    int64_t P, width;
+    float* out[3];
+    int64_t end[3];
+};
+
 // Each returns hipSuccess or the launch error; bf16 selects the input dtype.
+hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream);
+hipError_t launch_dropout(const DropoutCall& a, bool bf16, hipStream_t stream);
+hipError_t launch_block_norm_fwd(const BlockNormArgs& a, bool bf16, bool residual_bf16, hipStream_t stream);
+hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool bf16, bool residual_bf16, hipStream_t stream);
+hipError_t launch_mixer_epilogue_bwd(const EpilogueBwdArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_mixer_prologue_bwd(const PrologueBwdArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_mixer_prologue(const MixerArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_mixer_epilogue(const EpilogueArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_chunk_bwd(const BwdArgs& a, bool bf16, hipStream_t stream);

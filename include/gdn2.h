@@ -370,6 +370,162 @@ gdn2_status gdn2_mixer_epilogue(const void* o, const void* gate, const float* we
                                 int64_t rows, int32_t dv, float eps, int32_t gate_act,
                                 gdn2_dtype dtype, void* stream);
 
+/*
+ * The training operators around the recurrence: the gradients of the mixer
+ * prologue and epilogue, and the step from one block of a layer to the next
+ * (norms, gate, residual scale, dropout) with its gradients.  Together with
+ * gdn2_chunk_fwd and gdn2_chunk_bwd they run a layer forward and backward; the
+ * projections between them are plain matrix products.
+ *
+ * Dropout.  `dropout_p` in [0, 1] is rounded to threshold = floor(2^16 p + 1/2)
+ * units of 2^-16; an element is dropped (set to zero, whatever it holds) when
+ * its 16 random bits are below the threshold, and else multiplied by
+ * 2^16 / (2^16 - threshold), so the expectation is exact.  The bits of element
+ * d of row r come from Philox4x32 with ten rounds (Salmon, Moraes, Dror and
+ * Shaw, "Parallel Random Numbers: As Easy as 1, 2, 3", 2011): counter words
+ * (block low, block high, offset low, offset high) with
+ * block = r * ceil(D / 8) + d / 8, key words (seed low, seed high); element
+ * d % 8 takes the low (even) or high (odd) half of output word (d % 8) / 2.
+ * The mask depends on the position, the seed and the offset alone: it is never
+ * stored, the backward call remakes it, and gdn2_dropout and
+ * gdn2_block_norm_fwd draw the same one.  Calls that should draw different masks
+ * take different offsets (one per call) or seeds.  `offset_device` (NULL, or a
+ * DEVICE uint64, 8-byte aligned) is added to offset when the kernel runs, so a
+ * replayed graph draws new masks when the program advances it; the backward
+ * call has to see the value that the forward call saw.
+ */
+
+/* Gate of a block's output (gate_layout). */
+typedef enum gdn2_block_gate {
+    GDN2_BLOCK_GATE_NONE = 0,    /* gate is NULL                     */
+    GDN2_BLOCK_GATE_CHANNEL = 1, /* [D] FP32, shared by every row    */
+    GDN2_BLOCK_GATE_TOKEN = 2,   /* [rows] dtype, one value per row  */
+    GDN2_BLOCK_GATE_FULL = 3     /* [rows, D] dtype                  */
+} gdn2_block_gate;
+
+/*
+ * The step from one block to the next.  Per row (token) of D channels, with
+ * rms(z) = sqrt(mean(z^2) + eps):
+ *     n     = u / rms(u) * weight_post         (u itself without weight_post)
+ *     x_out = x + residual_scale * dropout(act(gate) * n)
+ *     h     = x_out / rms(x_out) * weight_pre
+ * u is a block's output, x the residual stream and h the next block's input.
+ * x_out is rounded to its type before the second norm: h is the norm of what is
+ * stored.  Decode is the same call with one row per sequence.
+ *
+ *   x, x_out : [rows, D] residual_dtype.  x_out may be x (in place).
+ *   u        : [rows, D] dtype, or NULL: then h is the norm of x, and x_out,
+ *              gate and weight_post must be NULL and dropout_p 0.
+ *   gate     : as gate_layout says; gate_act 0 = sigmoid, 1 = SiLU,
+ *              2 = the value itself (ignored without a gate).
+ *   weight_post, weight_pre : [D] FP32, or NULL (no such norm).
+ *   h        : [rows, D] dtype; NULL exactly when weight_pre is NULL.
+ *   residual_dtype is dtype, or FP32 with bf16 blocks (FP32 blocks with a bf16
+ *   stream: GDN2_ERR_BAD_DTYPE).  1 <= D <= 16384 (above: GDN2_ERR_UNSUPPORTED),
+ *   any D, at full speed for multiples of 8.  rows >= 0.  eps > 0.
+ * Outputs must not overlap inputs (but x_out = x) or each other.  The norms'
+ * sums are FP32, so rows of entries past 1e19 overflow to a norm of zero.
+ */
+gdn2_status gdn2_block_norm_fwd(const void* x, const void* u, const void* gate, const float* weight_post,
+                                const float* weight_pre, void* x_out, void* h, int64_t rows, int32_t D, float eps,
+                                float residual_scale, int32_t gate_layout, int32_t gate_act, double dropout_p,
+                                uint64_t seed, uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype,
+                                gdn2_dtype residual_dtype, void* stream);
+
+/*
+ * Gradients of gdn2_block_norm_fwd for the loss <d_x_out, x_out> + <d_h, h>.
+ *
+ *   x_out    : the stream the forward call stored (with u NULL: its x).  Needed
+ *              with weight_pre only, else ignored.
+ *   u, gate, weight_post, weight_pre, and the scalars: as in the forward call.
+ *   d_x_out  : [rows, D] residual_dtype, or NULL for zero.
+ *   d_h      : [rows, D] dtype; NULL exactly when weight_pre is NULL.  d_x_out and
+ *              d_h both NULL: GDN2_ERR_NULL_POINTER.
+ *   d_x      : [rows, D] residual_dtype.  May be d_x_out (in place).
+ *   d_u      : [rows, D] dtype; NULL exactly when u is NULL.
+ *   d_gate   : the gate's shape and type, or NULL if not wanted.
+ *   d_weight_post, d_weight_pre : [D] FP32, or NULL if not wanted.
+ *   A gradient of an input that is not given: GDN2_ERR_BAD_SHAPE.
+ *   workspace: gdn2_block_norm_bwd_workspace_bytes(rows, D) bytes of device
+ *              memory, 16-byte aligned, when d_weight_post, d_weight_pre or a
+ *              CHANNEL d_gate is wanted (else it may be NULL); contents on entry
+ *              do not matter.  Missing or smaller: GDN2_ERR_WORKSPACE.
+ * The gradient of a shared input is the sum over all that share it (zero when
+ * rows = 0).  Outputs and the workspace must not overlap inputs (but d_x =
+ * d_x_out) or each other.  Calls that may run at the same time need a workspace
+ * each.
+ */
+gdn2_status gdn2_block_norm_bwd(const void* x_out, const void* u, const void* gate, const float* weight_post,
+                                const float* weight_pre, const void* d_x_out, const void* d_h, void* d_x, void* d_u,
+                                void* d_gate, float* d_weight_post, float* d_weight_pre, int64_t rows, int32_t D,
+                                float eps, float residual_scale, int32_t gate_layout, int32_t gate_act,
+                                double dropout_p, uint64_t seed, uint64_t offset, const uint64_t* offset_device,
+                                gdn2_dtype dtype, gdn2_dtype residual_dtype, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Workspace of gdn2_block_norm_bwd: up to 1024 partial rows of 3 x D FP32 sums,
+ * rounded up to 256 bytes.  0 for invalid sizes and for rows = 0. */
+size_t gdn2_block_norm_bwd_workspace_bytes(int64_t rows, int32_t D);
+
+/*
+ * Dropout alone: y = dropout(x) over [rows, D] elements of dtype, with the mask
+ * described above.  A flat array is one row.  The operator is its own adjoint:
+ * the gradient is the same call on dy.  y may be x (in place), else it must
+ * not overlap it.  rows >= 0, D >= 1; ceil(D / 8) * rows below 2^56.
+ */
+gdn2_status gdn2_dropout(const void* x, void* y, int64_t rows, int64_t D, double dropout_p, uint64_t seed,
+                         uint64_t offset, const uint64_t* offset_device, gdn2_dtype dtype, void* stream);
+
+/*
+ * Gradients of gdn2_mixer_epilogue for the loss <d_y, y>.
+ *   o, gate, weight, rows, dv, eps, gate_act, dtype: the forward call's.
+ *   d_y, d_o, d_gate : [rows, dv] dtype.   d_weight : [dv] FP32, or NULL if not
+ *   wanted; with it a workspace of gdn2_mixer_epilogue_bwd_workspace_bytes bytes,
+ *   16-byte aligned (missing or smaller: GDN2_ERR_WORKSPACE).
+ * Outputs and the workspace must not overlap inputs or each other.
+ */
+gdn2_status gdn2_mixer_epilogue_bwd(const void* o, const void* gate, const float* weight, const void* d_y, void* d_o,
+                                    void* d_gate, float* d_weight, int64_t rows, int32_t dv, float eps,
+                                    int32_t gate_act, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Workspace of gdn2_mixer_epilogue_bwd: up to 1024 partial rows of dv FP32 sums,
+ * rounded up to 256 bytes.  0 for invalid sizes and for rows = 0. */
+size_t gdn2_mixer_epilogue_bwd_workspace_bytes(int64_t rows, int32_t dv);
+
+/*
+ * Gradients of gdn2_mixer_prologue for the loss <d_q, q> + <d_k, k> + <d_v, v> +
+ * <d_b, b> + <d_w, w> + <d_conv_state_out, conv_state_out>.
+ *
+ *   xq .. w_logit, conv_state_in, cu_seqlens and the scalars: the forward call's.
+ *   d_q, d_k, d_b : [B, T, H, dk] dtype      d_v, d_w : [B, T, H, dv] dtype
+ *   d_conv_state_out : [N, H * (2 dk + dv), K - 1] FP32, or NULL for zero.
+ *   d_xq, d_xk, d_b_logit : [B, T, H, dk] dtype   d_xv, d_w_logit : [B, T, H, dv]
+ *   d_conv_q, d_conv_k, d_conv_v : the filters' shapes, FP32, each NULL if not
+ *              wanted.
+ *   d_conv_state_in : like d_conv_state_out, or NULL if not wanted (it exists
+ *              also where conv_state_in was NULL: the gradient at zero).
+ *   workspace: gdn2_mixer_prologue_bwd_workspace_bytes bytes of device memory,
+ *              16-byte aligned, when a filter's gradient is wanted (else it may be
+ *              NULL).  Missing or smaller: GDN2_ERR_WORKSPACE.
+ * Outputs and the workspace must not overlap inputs or each other.
+ */
+gdn2_status gdn2_mixer_prologue_bwd(const void* xq, const void* xk, const void* xv, const float* conv_q,
+                                    const float* conv_k, const float* conv_v, const void* b_logit,
+                                    const void* w_logit, const float* conv_state_in, const void* d_q, const void* d_k,
+                                    const void* d_v, const void* d_b, const void* d_w, const float* d_conv_state_out,
+                                    void* d_xq, void* d_xk, void* d_xv, float* d_conv_q, float* d_conv_k,
+                                    float* d_conv_v, void* d_b_logit, void* d_w_logit, float* d_conv_state_in,
+                                    const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t dk,
+                                    int32_t dv, int32_t kernel_size, int32_t num_seqs, float q_scale, float eps_l2,
+                                    gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of gdn2_mixer_prologue_bwd: one partial row of H x (2 dk + dv) x K
+ * FP32 sums per run of tokens of a batch row, rounded up to 256 bytes.  0 for
+ * invalid sizes and for T = 0. */
+size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
+                                               int32_t kernel_size);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* gdn2_status_string(gdn2_status status);
 
