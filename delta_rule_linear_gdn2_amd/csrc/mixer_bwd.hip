@@ -24,6 +24,8 @@
 // K - 1 tokens after it, so a run reads that many tokens past its end (and
 // before its start).  The filters' gradients of a run go to the workspace and
 // are added by the column-sum kernel.
+#include <type_traits>
+
 #include "row_device.hpp"
 
 namespace gdn2 {
@@ -83,9 +85,9 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
         }
         Eight<T> out;
         out.put(d);
-        out.template store<true>(static_cast<T*>(a.d_o) + e, n);
+        out.template store<true, true>(static_cast<T*>(a.d_o) + e, n);
         out.put(dg);
-        out.template store<true>(static_cast<T*>(a.d_gate) + e, n);
+        out.template store<true, true>(static_cast<T*>(a.d_gate) + e, n);
     }
     if (!a.d_weight) return;
 #pragma unroll
@@ -105,6 +107,7 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
 }
 
 constexpr int64_t kEpiBlocks = 1024;
+constexpr int64_t kWantWaves = 4096;
 
 template <typename T>
 hipError_t epilogue_typed(const EpilogueBwdArgs& a, hipStream_t stream)
@@ -141,61 +144,109 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int32_t T, 
     return lo;
 }
 
-// CPL consecutive channels: eight as one group, four or two as half and
-// quarter of one.
+// CPL consecutive channels of a row, as loaded: eight, four or two (bf16 stays
+// packed until used).  They sit at a boundary of their own size.
+template <typename T, int CPL>
+struct Channels;
 template <int CPL>
-__device__ __forceinline__ void load_channels(const bf16raw* p, float* v)
-{
+struct Channels<bf16raw, CPL> {
+    typedef uint32_t raw_t __attribute__((ext_vector_type(CPL / 2 > 1 ? CPL / 2 : 2)));
+    uint32_t u[CPL / 2];
+    __device__ __forceinline__ void load(const bf16raw* p)
+    {
+        if (CPL == 2) {
+            u[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            const raw_t v = *reinterpret_cast<const raw_t*>(p);
 #pragma unroll
-    for (int j = 0; j < CPL / 2; ++j) {
-        const uint32_t u = reinterpret_cast<const uint32_t*>(p)[j];
-        v[2 * j] = __uint_as_float(u << 16);
-        v[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
+            for (int j = 0; j < CPL / 2; ++j) u[j] = v[j];
+        }
     }
-}
-template <int CPL>
-__device__ __forceinline__ void load_channels(const float* p, float* v)
-{
+    __device__ __forceinline__ void get(float* v) const
+    {
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) v[j] = p[j];
-}
-template <int CPL>
-__device__ __forceinline__ void store_channels(bf16raw* p, const float* v)
-{
+        for (int j = 0; j < CPL / 2; ++j) {
+            v[2 * j] = __uint_as_float(u[j] << 16);
+            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(bf16raw* p, const float* v)
+    {
+        if (CPL == 2) {
+            *reinterpret_cast<uint32_t*>(p) = f32x2_to_bf16x2(v[0], v[1]);
+        } else {
+            raw_t r;
 #pragma unroll
-    for (int j = 0; j < CPL / 2; ++j) reinterpret_cast<uint32_t*>(p)[j] = f32x2_to_bf16x2(v[2 * j], v[2 * j + 1]);
-}
+            for (int j = 0; j < CPL / 2; ++j) r[j] = f32x2_to_bf16x2(v[2 * j], v[2 * j + 1]);
+            put16<true>(p, r);
+        }
+    }
+};
 template <int CPL>
-__device__ __forceinline__ void store_channels(float* p, const float* v)
-{
+struct Channels<float, CPL> {
+    static constexpr int V = CPL < 4 ? CPL : 4;
+    typedef float raw_t __attribute__((ext_vector_type(V)));
+    float u[CPL];
+    __device__ __forceinline__ void load(const float* p)
+    {
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) p[j] = v[j];
-}
+        for (int i = 0; i < CPL / V; ++i) {
+            const raw_t v = reinterpret_cast<const raw_t*>(p)[i];
+#pragma unroll
+            for (int j = 0; j < V; ++j) u[i * V + j] = v[j];
+        }
+    }
+    __device__ __forceinline__ void get(float* v) const
+    {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) v[j] = u[j];
+    }
+    static __device__ __forceinline__ void store(float* p, const float* v)
+    {
+#pragma unroll
+        for (int i = 0; i < CPL / V; ++i) {
+            raw_t r;
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[j] = v[i * V + j];
+            put16<true>(p + i * V, r);
+        }
+    }
+};
+
+constexpr int channels_per_lane(int KM) { return KM <= 1 ? 8 : KM <= 4 ? 4 : 2; }
+constexpr int kStep = 4;  // tokens per unrolled step
 
 // One convolution path (PATH 0 q, 1 k, 2 v; head width D) of one wavefront's
-// run.  KM bounds the filter's taps: tap i of K sits at index KM - K + i, and
-// everything below index KM - K stays untouched.
+// run.  KM bounds the filter's taps (KM = K up to four): tap i of K sits at
+// index KM - K + i, and everything below index KM - K stays untouched.
+//
+// Tokens go kStep at a time with the next step's loads in flight; a step that a
+// sequence's start or end falls into goes token by token.  The window and the
+// unfinished gradients of a step are one array each, indexed by constants, so
+// nothing moves between registers inside a step.
 template <typename T, int D, int PATH, int KM>
 __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t wid, int lane)
 {
-    constexpr int CPL = KM <= 4 ? 8 : KM <= 8 ? 4 : 2;  // channels per lane
-    constexpr int LPH = D / CPL, HPW = 64 / LPH;        // lanes per head, heads per wavefront
-    constexpr int W = KM - 1;                           // window entries
+    constexpr int CPL = channels_per_lane(KM);
+    constexpr int LPH = D / CPL, HPW = 64 / LPH;  // lanes per head, heads per wavefront
+    constexpr int W = KM - 1;                     // window entries
+    using Ch = Channels<T, CPL>;
     const int ng = (a.H + HPW - 1) / HPW;
     const int64_t nruns = (int64_t(a.T) + a.run - 1) / a.run;
     if (wid >= int64_t(a.B) * nruns * ng) return;
     const int h = int(wid % ng) * HPW + lane / LPH;
     if (h >= a.H) return;  // lanes past the last head share no sum with live ones
     const int64_t run = (wid / ng) % nruns, brow = wid / ng / nruns;
-    const int64_t t0 = run * a.run, t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
-    const int K = a.K, low = KM - K;
-    const int chan = h * D + (lane % LPH) * CPL;        // first channel within the path
-    const int64_t stride = int64_t(a.H) * D, row0 = brow * a.T * stride + chan;
+    const int t0 = int(run * a.run), t1 = a.T - t0 > a.run ? t0 + a.run : a.T;
+    const int K = KM <= 4 ? KM : a.K, low = KM - K;
+    const int chan = h * D + (lane % LPH) * CPL;  // first channel within the path
+    const int64_t stride = int64_t(a.H) * D, row0 = brow * a.T * stride;
     const int64_t nch = int64_t(a.H) * (2 * a.dk + a.dv);
     const int64_t state_chan = int64_t(PATH) * a.H * a.dk + chan;  // q, k, v in turn
-    const T* x = static_cast<const T*>(a.x[PATH]);
-    const T* dout = static_cast<const T*>(a.d_out[PATH]);
-    T* dx = static_cast<T*>(a.d_x[PATH]);
+    // a token's address: a scalar and this lane's channel
+    const T* x = static_cast<const T*>(a.x[PATH]) + row0;
+    const T* dout = static_cast<const T*>(a.d_out[PATH]) + row0;
+    T* dx = static_cast<T*>(a.d_x[PATH]) + row0;
 
     float w[KM][CPL], dw[KM][CPL];
 #pragma unroll
@@ -212,9 +263,9 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
         n = sequence_of(a.cu_seqlens, a.N, a.T, t0);
         sequence_bounds(a.cu_seqlens, n, a.T, bos, eos, unused);
     }
-    // xw[j]: the input W - j positions before the current token; pend[j]: the
-    // gradient gathered so far for that position
-    float xw[W > 0 ? W : 1][CPL], pend[W > 0 ? W : 1][CPL];
+    // xw[j]: for j < W the input W - j positions before the step's first token,
+    // then the step's inputs; pend[j]: the gradient gathered for that position
+    float xw[W + kStep][CPL], pend[W + kStep][CPL];
     auto restart = [&](int64_t t) {
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -223,7 +274,9 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
             for (int c = 0; c < CPL; ++c) xw[j][c] = pend[j][c] = 0.f;
             if (j < low) continue;
             if (s >= bos) {
-                load_channels<CPL>(x + row0 + s * stride, xw[j]);
+                Ch r;
+                r.load(x + s * stride + chan);
+                r.get(xw[j]);
             } else if (a.conv_state_in) {
                 const int64_t js = (K - 1) - (bos - s);
                 if (js >= 0) {
@@ -237,7 +290,7 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
     // the finished gradient of position s of the current sequence
     auto finish = [&](int64_t s, const float* v) {
         if (s >= bos) {
-            if (s >= t0 && s < t1) store_channels<CPL>(dx + row0 + s * stride, v);
+            if (s >= t0 && s < t1) Ch::store(dx + s * stride + chan, v);
         } else if (a.d_state_in && bos >= t0 && bos < t1) {
             const int64_t js = (K - 1) - (bos - s);
             if (js >= 0) {
@@ -247,29 +300,23 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
             }
         }
     };
-    restart(t0);
-    for (int64_t t = t0; t < t1 + K - 1 && t < a.T; ++t) {
-        if (t >= eos) {  // the next non-empty sequence starts here (packed input only)
-            if (t >= t1) break;
-            n = sequence_of(a.cu_seqlens, a.N, a.T, t);
-            sequence_bounds(a.cu_seqlens, n, a.T, bos, eos, unused);
-            restart(t);
-        }
-        float xt[CPL], g[CPL], y[CPL], v[CPL], sg[CPL];
-        load_channels<CPL>(x + row0 + t * stride, xt);
-        load_channels<CPL>(dout + row0 + t * stride, g);
+    // token with its input at xw[W + i]: its part of the gradients
+    auto token = [&](int i, const float* g, bool mine) {
+        float v[CPL], dy[CPL];
         float ss = 0.f, sv = 0.f;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            float acc = w[W][c] * xt[c];
+            float y = w[W][c] * xw[W + i][c];
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (i >= low) acc = fmaf(w[i][c], xw[i][c], acc);
-            y[c] = acc;
-            sg[c] = fast_sigmoid(acc);
-            v[c] = acc * sg[c];
-            ss = fmaf(v[c], v[c], ss);
-            sv = fmaf(v[c], g[c], sv);
+            for (int j = 0; j < W; ++j)
+                if (j >= low) y = fmaf(w[j][c], xw[i + j][c], y);
+            const float sg = fast_sigmoid(y);
+            v[c] = y * sg;
+            dy[c] = fmaf(v[c], 1.f - sg, sg);  // SiLU'(y)
+            if (PATH < 2) {
+                ss = fmaf(v[c], v[c], ss);
+                sv = fmaf(v[c], g[c], sv);
+            }
         }
         float r = 1.f, back = 0.f;
         if (PATH < 2) {
@@ -282,47 +329,112 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
                 back *= a.q_scale;
             }
         }
-        const bool mine = t < t1;
-        float done[CPL];
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            const float dv = PATH < 2 ? r * g[c] - v[c] * back : g[c];
-            const float dy = dv * sg[c] * (1.f + y[c] * (1.f - sg[c]));
-            if (mine) {
+            dy[c] *= PATH < 2 ? r * g[c] - v[c] * back : g[c];
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if (i >= low) dw[i][c] = fmaf(dy, xw[i][c], dw[i][c]);
-                dw[W][c] = fmaf(dy, xt[c], dw[W][c]);
-            }
-            // position W - j back gets w[j] dy; the oldest one is then finished, the others move one back
-            done[c] = w[W][c] * dy;
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if (j < low) continue;
-                const float p = fmaf(w[j][c], dy, pend[j][c]);
-                if (j == low) done[c] = p;
-                else pend[j - 1][c] = p;
-                if (j > low) xw[j - 1][c] = xw[j][c];
-            }
-            if (W > 0 && low < W) {
-                pend[W - 1][c] = w[W][c] * dy;
-                xw[W - 1][c] = xt[c];
-            }
+            for (int j = 0; j < W; ++j)
+                if (j >= low) pend[i + j][c] = fmaf(w[j][c], dy[c], pend[i + j][c]);
+            pend[i + W][c] = w[W][c] * dy[c];
         }
-        finish(t - (K - 1), done);
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (j >= low) {
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c) dw[j][c] = fmaf(dy[c], xw[i + j][c], dw[j][c]);
+                }
+        }
+    };
+    // the window and the unfinished gradients `by` tokens on
+    auto advance = [&](auto by) {
+        constexpr int S = decltype(by)::value;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                xw[j][c] = j >= low ? xw[j + S][c] : 0.f;
+                pend[j][c] = pend[j + S][c];
+            }
+    };
+
+    const int last = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;  // tokens past t1 complete this run's gradients
+    // a whole step inside one sequence, neither its first K - 1 tokens nor its last one
+    auto whole = [&](int64_t t) { return t + kStep <= last && t + kStep < eos && t - (K - 1) >= bos; };
+    Ch rx[kStep], rg[kStep];
+    auto load_step = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            rx[i].load(x + (t + i) * stride + chan);
+            rg[i].load(dout + (t + i) * stride + chan);
+        }
+    };
+    restart(t0);
+    int64_t ahead = -1;  // the step whose loads are in flight
+    for (int64_t t = t0; t < last;) {
+        if (whole(t)) {
+            if (ahead != t) load_step(t);
+            Ch g[kStep];
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                rx[i].get(xw[W + i]);
+                g[i] = rg[i];
+            }
+            if (whole(t + kStep)) {
+                load_step(t + kStep);
+                ahead = t + kStep;
+            }
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                float gi[CPL];
+                g[i].get(gi);
+                token(i, gi, t + i < t1);
+                __builtin_amdgcn_sched_barrier(0);  // tokens interleaved would hold more registers at once
+                // position t + i - (K - 1) is inside the sequence and before t1
+                if (t + i - (K - 1) >= t0) {
+                    if (KM <= 4) {
+                        Ch::store(dx + (t + i - (K - 1)) * stride + chan, pend[i]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < KM; ++j)
+                            if (j == low) Ch::store(dx + (t + i - (K - 1)) * stride + chan, pend[i + j]);
+                    }
+                }
+            }
+            advance(std::integral_constant<int, kStep>{});
+            t += kStep;
+            continue;
+        }
+        if (t >= eos) {  // the next non-empty sequence starts here (packed input only)
+            if (t >= t1) break;
+            n = sequence_of(a.cu_seqlens, a.N, a.T, t);
+            sequence_bounds(a.cu_seqlens, n, a.T, bos, eos, unused);
+            restart(t);
+        }
+        Ch one;
+        float g[CPL];
+        one.load(x + t * stride + chan);
+        one.get(xw[W]);
+        one.load(dout + t * stride + chan);
+        one.get(g);
+        token(0, g, t < t1);
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+            if (j == low) finish(t - (K - 1), pend[j]);
+        advance(std::integral_constant<int, 1>{});
         if (t == eos - 1) {  // no later token adds to the last K - 1 positions
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 if (j < low) continue;
-                const int64_t s = t + 1 - W + j;
                 float p[CPL];
 #pragma unroll
                 for (int c = 0; c < CPL; ++c)
                     p[c] = pend[j][c] +
                            (a.d_state_out ? a.d_state_out[(int64_t(n) * nch + state_chan + c) * (K - 1) + (j - low)] : 0.f);
-                finish(s, p);
+                finish(t + 1 - W + j, p);
             }
         }
+        ++t;
     }
     if (a.partial) {
         float* out = a.partial + ((brow * nruns + run) * nch + state_chan) * K;
@@ -334,11 +446,12 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
     }
 }
 
-// Gate logits: eight channels a lane over the wavefront's run.
+// Gate logits: eight channels a lane over the wavefront's run, eight tokens'
+// loads at a time.
 template <typename T, int D, int WHICH>
 __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t wid, int lane)
 {
-    constexpr int LPH = D / 8, HPW = 64 / LPH;
+    constexpr int LPH = D / 8, HPW = 64 / LPH, M = sizeof(T) == 2 ? 8 : 4;
     const int ng = (a.H + HPW - 1) / HPW;
     const int64_t nruns = (int64_t(a.T) + a.run - 1) / a.run;
     if (wid >= int64_t(a.B) * nruns * ng) return;
@@ -346,98 +459,96 @@ __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t 
     if (h >= a.H) return;
     const int64_t run = (wid / ng) % nruns, brow = wid / ng / nruns;
     const int64_t t0 = run * a.run, t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
-    const int64_t stride = int64_t(a.H) * D, row0 = brow * a.T * stride + h * D + (lane % LPH) * 8;
+    const int64_t stride = int64_t(a.H) * D, row0 = brow * a.T * stride;
+    const int chan = h * D + (lane % LPH) * 8;
     const T* logit = static_cast<const T*>(a.logit[WHICH]) + row0;
     const T* dg = static_cast<const T*>(a.d_gate[WHICH]) + row0;
     T* out = static_cast<T*>(a.d_logit[WHICH]) + row0;
-    for (int64_t t = t0; t < t1; ++t) {
-        Eight<T> rl, rd;
-        rl.template load<true>(logit + t * stride, 8);
-        rd.template load<true>(dg + t * stride, 8);
-        float l[8], d[8];
-        rl.get(l);
-        rd.get(d);
+    for (int64_t t = t0; t < t1; t += M) {
+        Eight<T> rl[M], rd[M];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float s = fast_sigmoid(l[j]);
-            d[j] *= s * (1.f - s);
+        for (int i = 0; i < M; ++i) {
+            const int64_t at = (t + i < t1 ? t + i : t1 - 1) * stride;
+            rl[i].template load<true>(logit + at + chan, 8);
+            rd[i].template load<true>(dg + at + chan, 8);
         }
-        rd.put(d);
-        rd.template store<true>(out + t * stride, 8);
-    }
-}
-
-// blockIdx.y + first: 0 q, 1 k, 2 b (head width dk), 3 v, 4 w (dv).  One launch
-// takes all five where dk = dv, else one takes the first three and one the rest.
-template <typename T, int D, int KM>
-__global__ __launch_bounds__(kThreads) void prologue_bwd_kernel(PrologueBwdArgs a, int first)
-{
-    const int lane = threadIdx.x % 64;
-    const int64_t wid = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
-    switch (blockIdx.y + first) {
-        case 0: conv_bwd_path<T, D, 0, KM>(a, wid, lane); break;
-        case 1: conv_bwd_path<T, D, 1, KM>(a, wid, lane); break;
-        case 2: gate_bwd_path<T, D, 0>(a, wid, lane); break;
-        case 3: conv_bwd_path<T, D, 2, KM>(a, wid, lane); break;
-        default: gate_bwd_path<T, D, 1>(a, wid, lane); break;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            if (t + i >= t1) break;
+            float l[8], d[8];
+            rl[i].get(l);
+            rd[i].get(d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float s = fast_sigmoid(l[j]);
+                d[j] *= s * (1.f - s);
+            }
+            rd[i].put(d);
+            rd[i].template store<true, true>(out + (t + i) * stride + chan, 8);
+        }
     }
 }
 
 // Sequences without tokens carry their state through, and its gradient back.
-__global__ __launch_bounds__(kThreads) void state_grad_passthrough_kernel(PrologueBwdArgs a)
+__device__ __forceinline__ void empty_sequences_path(const PrologueBwdArgs& a)
 {
-    const int64_t per = int64_t(a.H) * (2 * a.dk + a.dv) * (a.K - 1);
-    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= int64_t(a.N) * per) return;
-    int64_t bos, eos, brow;
-    sequence_bounds(a.cu_seqlens, int(i / per), a.T, bos, eos, brow);
-    if (eos > bos) return;
-    a.d_state_in[i] = a.d_state_out ? a.d_state_out[i] : 0.f;
+    const int64_t per = int64_t(a.H) * (2 * a.dk + a.dv) * (a.K - 1), total = int64_t(a.N) * per;
+    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += int64_t(gridDim.x) * kThreads) {
+        int64_t bos, eos, brow;
+        sequence_bounds(a.cu_seqlens, int(i / per), a.T, bos, eos, brow);
+        if (eos <= bos) a.d_state_in[i] = a.d_state_out ? a.d_state_out[i] : 0.f;
+    }
 }
 
-template <typename T, int D>
-hipError_t prologue_paths(const PrologueBwdArgs& a, int first, int count, hipStream_t stream)
+// blockIdx.y: 0 q, 1 k, 2 v, 3 b, 4 w, 5 the empty sequences.  The head width is
+// looked up here, so a call is one launch whether or not dk = dv.
+template <typename T, int KM>
+__global__ __launch_bounds__(kThreads) void prologue_bwd_kernel(PrologueBwdArgs a)
 {
-    const int cpl = a.K <= 4 ? 8 : a.K <= 8 ? 4 : 2, hpw = 64 / (D / cpl);
-    const int64_t waves = int64_t(a.B) * ((int64_t(a.T) + a.run - 1) / a.run) * ((a.H + hpw - 1) / hpw);
-    const int64_t blocks = (waves + 3) / 4;
-    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const dim3 grid{unsigned(blocks), unsigned(count), 1}, block{kThreads, 1, 1};
-    if (a.K == 1)
-        hipLaunchKernelGGL((prologue_bwd_kernel<T, D, 1>), grid, block, 0, stream, a, first);
-    else if (a.K <= 4)
-        hipLaunchKernelGGL((prologue_bwd_kernel<T, D, 4>), grid, block, 0, stream, a, first);
-    else if (a.K <= 8)
-        hipLaunchKernelGGL((prologue_bwd_kernel<T, D, 8>), grid, block, 0, stream, a, first);
-    else
-        hipLaunchKernelGGL((prologue_bwd_kernel<T, D, 16>), grid, block, 0, stream, a, first);
-    return hipGetLastError();
-}
-
-template <typename T>
-hipError_t prologue_width(const PrologueBwdArgs& a, int d, int first, int count, hipStream_t stream)
-{
-    switch (d) {
-        case 32: return prologue_paths<T, 32>(a, first, count, stream);
-        case 64: return prologue_paths<T, 64>(a, first, count, stream);
-        case 128: return prologue_paths<T, 128>(a, first, count, stream);
-        default: return hipErrorInvalidValue;
+    const int lane = threadIdx.x % 64;
+    // the same in every lane, so runs, sequences and addresses are scalars
+    const int64_t wid = int64_t(blockIdx.x) * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    switch (blockIdx.y * 256 + (blockIdx.y == 2 || blockIdx.y == 4 ? a.dv : a.dk)) {
+        case 32: conv_bwd_path<T, 32, 0, KM>(a, wid, lane); break;
+        case 64: conv_bwd_path<T, 64, 0, KM>(a, wid, lane); break;
+        case 128: conv_bwd_path<T, 128, 0, KM>(a, wid, lane); break;
+        case 256 + 32: conv_bwd_path<T, 32, 1, KM>(a, wid, lane); break;
+        case 256 + 64: conv_bwd_path<T, 64, 1, KM>(a, wid, lane); break;
+        case 256 + 128: conv_bwd_path<T, 128, 1, KM>(a, wid, lane); break;
+        case 512 + 32: conv_bwd_path<T, 32, 2, KM>(a, wid, lane); break;
+        case 512 + 64: conv_bwd_path<T, 64, 2, KM>(a, wid, lane); break;
+        case 512 + 128: conv_bwd_path<T, 128, 2, KM>(a, wid, lane); break;
+        case 768 + 32: gate_bwd_path<T, 32, 0>(a, wid, lane); break;
+        case 768 + 64: gate_bwd_path<T, 64, 0>(a, wid, lane); break;
+        case 768 + 128: gate_bwd_path<T, 128, 0>(a, wid, lane); break;
+        case 1024 + 32: gate_bwd_path<T, 32, 1>(a, wid, lane); break;
+        case 1024 + 64: gate_bwd_path<T, 64, 1>(a, wid, lane); break;
+        case 1024 + 128: gate_bwd_path<T, 128, 1>(a, wid, lane); break;
+        default: empty_sequences_path(a); break;
     }
 }
 
 template <typename T>
 hipError_t prologue_typed(const PrologueBwdArgs& a, hipStream_t stream)
 {
-    if (a.T > 0) {
-        hipError_t e = prologue_width<T>(a, a.dk, 0, a.dk == a.dv ? 5 : 3, stream);
-        if (e == hipSuccess && a.dk != a.dv) e = prologue_width<T>(a, a.dv, 3, 2, stream);
-        if (e != hipSuccess) return e;
-    }
-    if (a.d_state_in && a.K > 1 && (a.cu_seqlens || a.T == 0)) {
-        const int64_t n = int64_t(a.N) * a.H * (2 * a.dk + a.dv) * (a.K - 1);
-        const int64_t blocks = (n + kThreads - 1) / kThreads;
+    const bool empties = a.d_state_in && a.K > 1 && (a.cu_seqlens || a.T == 0);
+    if (a.T > 0 || empties) {
+        const int d = a.dk > a.dv ? a.dk : a.dv, hpw = 64 / (d / channels_per_lane(a.K));
+        const int64_t waves = int64_t(a.B) * ((int64_t(a.T) + a.run - 1) / a.run) * ((a.H + hpw - 1) / hpw);
+        const int64_t blocks = waves > 0 ? (waves + 3) / 4 : 1;
         if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL(state_grad_passthrough_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, stream, a);
+        const dim3 grid{unsigned(blocks), empties ? 6u : 5u, 1}, block{kThreads, 1, 1};
+#define GDN2_TAPS(KM) hipLaunchKernelGGL((prologue_bwd_kernel<T, KM>), grid, block, 0, stream, a)
+        switch (a.K) {
+            case 1: GDN2_TAPS(1); break;
+            case 2: GDN2_TAPS(2); break;
+            case 3: GDN2_TAPS(3); break;
+            case 4: GDN2_TAPS(4); break;
+            default:
+                if (a.K <= 8) GDN2_TAPS(8);
+                else GDN2_TAPS(16);
+        }
+#undef GDN2_TAPS
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -459,8 +570,12 @@ int64_t epilogue_bwd_partials(int64_t rows, int32_t dv)
 
 int32_t prologue_bwd_run(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t K)
 {
-    (void)B, (void)T, (void)H, (void)dk, (void)dv, (void)K;
-    return 64;
+    const int cpl = channels_per_lane(K), d = dk < dv ? dk : dv, hpw = 64 / (d / cpl);
+    const int64_t per_run = 3 * int64_t(B) * ((H + hpw - 1) / hpw);  // convolution wavefronts
+    int32_t steps = 32;
+    while (steps > (K <= 4 ? 4 : 8) && per_run * ((int64_t(T) + steps * kStep - K) / (steps * kStep - (K - 1))) < kWantWaves)
+        steps /= 2;
+    return steps * kStep - (K - 1);
 }
 
 hipError_t launch_mixer_epilogue_bwd(const EpilogueBwdArgs& a, bool bf16, hipStream_t stream)

@@ -40,6 +40,9 @@ __device__ __forceinline__ float group_sum(float x)
 // It keeps its limits: 0 and 1 at minus and plus infinity, NaN for NaN.
 __device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
+// STREAM in a store: past the caches, for outputs that no cache will hold until
+// they are read.
+//
 // Eight consecutive elements of a row as loaded (bf16 stays packed until used).
 // FULL: the eight exist and sit at a 16-byte boundary.  Otherwise n of them
 // exist (n <= 0: none) and the address is aligned to the element only: gfx950
@@ -49,6 +52,13 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));
 typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+
+template <bool STREAM, typename V, typename P>
+__device__ __forceinline__ void put16(P* p, const V& v)
+{
+    if (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+    else *reinterpret_cast<V*>(p) = v;
+}
 
 template <typename T>
 struct Eight;
@@ -86,11 +96,11 @@ struct Eight<bf16raw> {
         u = u32x4_t{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
                     f32x2_to_bf16x2(v[6], v[7])};
     }
-    template <bool FULL>
+    template <bool FULL, bool STREAM = false>
     __device__ __forceinline__ void store(bf16raw* p, int n) const
     {
         if (FULL) {
-            if (n > 0) *reinterpret_cast<u32x4_t*>(p) = u;
+            if (n > 0) put16<STREAM>(p, u);
             return;
         }
         if (n >= 8) {
@@ -145,13 +155,13 @@ struct Eight<float> {
             b[j] = v[4 + j];
         }
     }
-    template <bool FULL>
+    template <bool FULL, bool STREAM = false>
     __device__ __forceinline__ void store(float* p, int n) const
     {
         if (FULL) {
             if (n > 0) {
-                *reinterpret_cast<f32x4_t*>(p) = a;
-                *reinterpret_cast<f32x4_t*>(p + 4) = b;
+                put16<STREAM>(p, a);
+                put16<STREAM>(p + 4, b);
             }
             return;
         }
