@@ -530,36 +530,48 @@ def _on_stream(f):
                 raise ValueError(f"stream: on {stream.device}, the tensors are on {first.device}")
             with torch.cuda.stream(stream):
                 return f(first, *args, **kw)
-        if first.is_cuda and first.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
+        index = first.get_device()
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return f(first, *args, **kw)
         return f(first, *args, **kw)
 
     return call
 
 
-def _run(name, dev, *args):
-    """Calls the C function on the current stream; raises what it refuses."""
+def _run(name, index, *args):
+    """Calls the C function on device ``index``'s current stream (its handle
+    alone: building the stream object takes longer than all checks); raises
+    what it refuses."""
     import torch
 
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a GPU (got {dev})")
-    rc = getattr(load(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if index < 0:
+        raise ValueError(f"{name}: tensors must be on a GPU")
+    rc = getattr(_LIB or load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != GDN2_OK:
         raise Gdn2Error(rc, name)
+
+
+def _expect(name, t, shape, dtype, index):
+    """_check at a fifth of its time where nothing is wrong."""
+    if not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        import torch
+
+        _check(name, t, tuple(shape), dtype, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _buffer(name, t, shape, dtype, dev):
-    """The caller's output tensor, checked, or a new one."""
-    import torch
-
+def _buffer(name, t, like, shape, dtype, index):
+    """The caller's output tensor, checked, or a new one like ``like`` (of that
+    shape, type and device)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _check(name, t, shape, dtype, dev)
+        import torch
+
+        return torch.empty_like(like)
+    _expect(name, t, shape, dtype, index)
     return t
 
 
@@ -577,23 +589,23 @@ def _workspace(t, nbytes, dev):
     return t, t.numel()
 
 
-def _rows(name, t):
-    if t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{name}: needs a last axis of at least one element (shape {tuple(t.shape)})")
+def _rows(name, t, shape):
+    if not shape or shape[-1] < 1:
+        raise ValueError(f"{name}: needs a last axis of at least one element (shape {tuple(shape)})")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return t.numel() // t.shape[-1]
+    return t.numel() // shape[-1]
 
 
-def _random(seed, offset, offset_device, dev):
+def _random(seed, offset, offset_device, index):
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"seed and offset must be in [0, 2^64) (got {seed}, {offset})")
+    if offset_device is None:
+        return seed, offset, None
     import torch
 
-    for name, v in (("seed", seed), ("offset", offset)):
-        if not 0 <= v < 1 << 64:
-            raise ValueError(f"{name}: {v} is not in [0, 2^64)")
-    if offset_device is not None:
-        _check("offset_device", offset_device, (1,), torch.int64, dev)
-    return seed, offset, _addr(offset_device)
+    _expect("offset_device", offset_device, (1,), torch.int64, index)
+    return seed, offset, offset_device.data_ptr()
 
 
 GATE_LAYOUTS = {"none": 0, "channel": 1, "token": 2, "full": 3}
@@ -602,27 +614,32 @@ BLOCK_GATE_ACTS = {"sigmoid": 0, "silu": 1, "identity": 2}
 
 def _block_inputs(x, u, gate, gate_layout, gate_act, weight_post, weight_pre):
     """Checks the inputs that the block norm's two directions share; returns
-    their sizes, types and codes."""
+    their rows, shape and device index, and the codes of gate and activation."""
     import torch
 
-    rows, shape, dev, rdt = _rows("x", x), tuple(x.shape), x.device, x.dtype
+    shape, index = x.shape, x.get_device()
+    rows = _rows("x", x, shape)
     if u is not None:
-        _check("u", u, shape, u.dtype, dev)
-    if gate_layout not in GATE_LAYOUTS:
+        _expect("u", u, shape, u.dtype, index)
+    layout, act = GATE_LAYOUTS.get(gate_layout), BLOCK_GATE_ACTS.get(gate_act)
+    if layout is None:
         raise ValueError(f"gate_layout must be one of {tuple(GATE_LAYOUTS)}")
-    if gate_act not in BLOCK_GATE_ACTS:
+    if act is None:
         raise ValueError(f"gate_act must be one of {tuple(BLOCK_GATE_ACTS)}")
-    if (gate is None) != (gate_layout == "none"):
-        raise ValueError(f"gate_layout {gate_layout!r} {'needs a' if gate is None else 'takes no'} gate")
-    if gate is not None and u is not None:
-        if gate_layout == "channel":
-            _check("gate", gate, shape[-1:], torch.float32, dev)
-        else:
-            _check("gate", gate, shape if gate_layout == "full" else shape[:-1], u.dtype, dev)
-    for name, w in (("weight_post", weight_post), ("weight_pre", weight_pre)):
-        if w is not None:
-            _check(name, w, shape[-1:], torch.float32, dev)
-    return rows, shape, dev, rdt, GATE_LAYOUTS[gate_layout], BLOCK_GATE_ACTS[gate_act]
+    if gate is None:
+        if layout:
+            raise ValueError(f"gate_layout {gate_layout!r} needs a gate")
+    elif layout == 1:
+        _expect("gate", gate, shape[-1:], torch.float32, index)
+    elif not layout:
+        raise ValueError("a gate needs a gate_layout")
+    elif u is not None:
+        _expect("gate", gate, shape if layout == 3 else shape[:-1], u.dtype, index)
+    if weight_post is not None:
+        _expect("weight_post", weight_post, shape[-1:], torch.float32, index)
+    if weight_pre is not None:
+        _expect("weight_pre", weight_pre, shape[-1:], torch.float32, index)
+    return rows, shape, index, layout, act
 
 
 @_on_stream
@@ -646,27 +663,30 @@ def gdn2_block_norm_fwd(x, u=None, *, gate=None, gate_layout="none", gate_act="s
     (default x's).  x_out may be x (in place); x_out and h are allocated when not
     given.
     """
-    import torch
-
-    rows, shape, dev, rdt, layout, act = _block_inputs(x, u, gate, gate_layout, gate_act, weight_post, weight_pre)
+    rows, shape, index, layout, act = _block_inputs(x, u, gate, gate_layout, gate_act, weight_post, weight_pre)
+    rdt = x.dtype
     dt = u.dtype if u is not None else dtype or rdt
-    code, rcode = _dtype_code(dt), _dtype_code(rdt)
     if u is not None:
-        x_out = _buffer("x_out", x_out, shape, rdt, dev)
+        x_out = _buffer("x_out", x_out, x, shape, rdt, index)
     elif x_out is not None:
         raise ValueError("x_out: there is none without u")
-    if weight_pre is not None:
-        h = _buffer("h", h, shape, dt, dev)
-    elif h is not None:
-        raise ValueError("h: there is none without weight_pre")
-    _run("gdn2_block_norm_fwd", dev, x.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
+    if weight_pre is None:
+        if h is not None:
+            raise ValueError("h: there is none without weight_pre")
+    elif u is not None:
+        h = _buffer("h", h, u, shape, dt, index)
+    elif h is None:
+        h = x.new_empty(shape, dtype=dt)
+    else:
+        _expect("h", h, shape, dt, index)
+    _run("gdn2_block_norm_fwd", index, x.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
          _addr(x_out), _addr(h), rows, shape[-1], eps, residual_scale, layout, act, dropout_p,
-         *_random(seed, offset, offset_device, dev), code, rcode)
+         *_random(seed, offset, offset_device, index), _dtype_code(dt), _dtype_code(rdt))
     return (x if u is None else x_out), h
 
 
 def gdn2_block_norm_bwd_workspace_bytes(rows, D) -> int:
-    return int(load().gdn2_block_norm_bwd_workspace_bytes(rows, D))
+    return int((_LIB or load()).gdn2_block_norm_bwd_workspace_bytes(rows, D))
 
 
 @_on_stream
@@ -684,30 +704,33 @@ def gdn2_block_norm_bwd(x_out, u, d_x_out, d_h, *, gate=None, gate_layout="none"
     """
     import torch
 
-    rows, shape, dev, rdt, layout, act = _block_inputs(x_out, u, gate, gate_layout, gate_act, weight_post, weight_pre)
-    D = shape[-1]
+    rows, shape, index, layout, act = _block_inputs(x_out, u, gate, gate_layout, gate_act, weight_post, weight_pre)
+    D, rdt = shape[-1], x_out.dtype
     dt = u.dtype if u is not None else d_h.dtype if d_h is not None else rdt
-    code, rcode = _dtype_code(dt), _dtype_code(rdt)
+    code = _dtype_code(dt)
     if d_x_out is not None:
-        _check("d_x_out", d_x_out, shape, rdt, dev)
+        _expect("d_x_out", d_x_out, shape, rdt, index)
     if (d_h is None) != (weight_pre is None):
         raise ValueError("d_h and weight_pre: both or neither")
     if d_h is not None:
-        _check("d_h", d_h, shape, dt, dev)
-    d_x = _buffer("d_x", d_x, shape, rdt, dev)
+        _expect("d_h", d_h, shape, dt, index)
+    d_x = _buffer("d_x", d_x, x_out, shape, rdt, index)
     if u is not None:
-        d_u = _buffer("d_u", d_u, shape, dt, dev)
-    if gate is not None and want_d_gate:
-        d_gate = _buffer("d_gate", d_gate, tuple(gate.shape), gate.dtype, dev)
-    want = want_d_weights
-    d_post = torch.empty(D, dtype=torch.float32, device=dev) if want and weight_post is not None else None
-    d_pre = torch.empty(D, dtype=torch.float32, device=dev) if want and weight_pre is not None else None
-    sums = d_post is not None or d_pre is not None or (d_gate is not None and gate_layout == "channel")
-    workspace, ws_bytes = _workspace(workspace, gdn2_block_norm_bwd_workspace_bytes(rows, D) if sums else 0, dev)
-    _run("gdn2_block_norm_bwd", dev, x_out.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
+        d_u = _buffer("d_u", d_u, u, shape, dt, index)
+    elif d_u is not None:
+        raise ValueError("d_u: there is none without u")
+    if gate is None or not want_d_gate:
+        d_gate = None
+    else:
+        d_gate = _buffer("d_gate", d_gate, gate, gate.shape, gate.dtype, index)
+    d_post = torch.empty_like(weight_post) if want_d_weights and weight_post is not None else None
+    d_pre = torch.empty_like(weight_pre) if want_d_weights and weight_pre is not None else None
+    sums = d_post is not None or d_pre is not None or (d_gate is not None and layout == 1)
+    workspace, ws_bytes = _workspace(workspace, gdn2_block_norm_bwd_workspace_bytes(rows, D) if sums else 0, x_out.device)
+    _run("gdn2_block_norm_bwd", index, x_out.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
          _addr(d_x_out), _addr(d_h), d_x.data_ptr(), _addr(d_u), _addr(d_gate), _addr(d_post), _addr(d_pre), rows, D,
-         eps, residual_scale, layout, act, dropout_p, *_random(seed, offset, offset_device, dev), code, rcode,
-         _addr(workspace), ws_bytes)
+         eps, residual_scale, layout, act, dropout_p, *_random(seed, offset, offset_device, index), code,
+         _dtype_code(rdt), _addr(workspace), ws_bytes)
     return {"d_x": d_x, "d_u": d_u, "d_gate": d_gate, "d_weight_post": d_post, "d_weight_pre": d_pre}
 
 
@@ -719,11 +742,11 @@ def gdn2_dropout(x, p, seed, offset=0, *, offset_device=None, out=None):
     2^-16; kept elements are divided by 1 - p.  offset_device: [1] int64 on the
     device, added to offset when the kernel runs (replayed graphs), or None.
     ``out`` may be x (in place)."""
-    rows, dev = _rows("x", x), x.device
-    code = _dtype_code(x.dtype)
-    out = _buffer("out", out, tuple(x.shape), x.dtype, dev)
-    _run("gdn2_dropout", dev, x.data_ptr(), out.data_ptr(), rows, x.shape[-1], p,
-         *_random(seed, offset, offset_device, dev), code)
+    shape, index, dt = x.shape, x.get_device(), x.dtype
+    rows = _rows("x", x, shape)
+    out = _buffer("out", out, x, shape, dt, index)
+    _run("gdn2_dropout", index, x.data_ptr(), out.data_ptr(), rows, shape[-1], p,
+         *_random(seed, offset, offset_device, index), _dtype_code(dt))
     return out
 
 
@@ -738,18 +761,19 @@ def gdn2_mixer_epilogue_bwd(o, gate, weight, d_y, *, eps=1e-5, act="sigmoid", wa
     allocated when not given."""
     import torch
 
-    rows, dv, shape, dev, dt = _rows("o", o), o.shape[-1], tuple(o.shape), o.device, o.dtype
-    code = _dtype_code(dt)
-    _check("gate", gate, shape, dt, dev)
-    _check("weight", weight, (dv,), torch.float32, dev)
-    _check("d_y", d_y, shape, dt, dev)
+    shape, index, dt = o.shape, o.get_device(), o.dtype
+    rows = _rows("o", o, shape)
+    dv, code = shape[-1], _dtype_code(dt)
+    _expect("gate", gate, shape, dt, index)
+    _expect("weight", weight, shape[-1:], torch.float32, index)
+    _expect("d_y", d_y, shape, dt, index)
     if act not in GATE_ACTS:
         raise ValueError(f"act must be one of {tuple(GATE_ACTS)}")
     d_o, d_gate = torch.empty_like(o), torch.empty_like(o)
     d_weight = torch.empty_like(weight) if want_d_weight else None
     workspace, ws_bytes = _workspace(workspace, gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv) if want_d_weight else 0,
-                                     dev)
-    _run("gdn2_mixer_epilogue_bwd", dev, o.data_ptr(), gate.data_ptr(), weight.data_ptr(), d_y.data_ptr(),
+                                     o.device)
+    _run("gdn2_mixer_epilogue_bwd", index, o.data_ptr(), gate.data_ptr(), weight.data_ptr(), d_y.data_ptr(),
          d_o.data_ptr(), d_gate.data_ptr(), _addr(d_weight), rows, dv, eps, GATE_ACTS[act], code, _addr(workspace),
          ws_bytes)
     return {"d_o": d_o, "d_gate": d_gate, "d_weight": d_weight}
@@ -775,34 +799,34 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
     """
     import torch
 
-    B, T, H, dk = xq.shape
-    dv = xv.shape[-1]
-    K = conv_q.shape[-1]
-    dev, dt = xq.device, xq.dtype
-    code = _dtype_code(dt)
-    N = B if cu_seqlens is None else int(cu_seqlens.shape[0]) - 1
-    for name, t, width in (("xq", xq, dk), ("xk", xk, dk), ("b_logit", b_logit, dk), ("xv", xv, dv),
-                           ("w_logit", w_logit, dv), ("d_q", d_q, dk), ("d_k", d_k, dk), ("d_b", d_b, dk),
-                           ("d_v", d_v, dv), ("d_w", d_w, dv)):
-        _check(name, t, (B, T, H, width), dt, dev)
+    key, value, index, dt = xq.shape, xv.shape, xq.get_device(), xq.dtype
+    if len(key) != 4 or len(value) != 4:
+        raise ValueError(f"xq, xk, xv: [B, T, H, d] (got {tuple(key)}, {tuple(value)})")
+    B, T, H, dk = key
+    dv, K, code = value[3], conv_q.shape[-1], _dtype_code(dt)
+    N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    for name, t in (("xq", xq), ("xk", xk), ("b_logit", b_logit), ("d_q", d_q), ("d_k", d_k), ("d_b", d_b)):
+        _expect(name, t, key, dt, index)
+    for name, t in (("xv", xv), ("w_logit", w_logit), ("d_v", d_v), ("d_w", d_w)):
+        _expect(name, t, (B, T, H, dv), dt, index)
     for name, t, width in (("conv_q", conv_q, dk), ("conv_k", conv_k, dk), ("conv_v", conv_v, dv)):
-        _check(name, t, (H * width, K), torch.float32, dev)
+        _expect(name, t, (H * width, K), torch.float32, index)
     st_shape = (N, H * (2 * dk + dv), K - 1)
     for name, t in (("conv_state", conv_state), ("d_conv_state_out", d_conv_state_out)):
         if t is not None:
-            _check(name, t, st_shape, torch.float32, dev)
+            _expect(name, t, st_shape, torch.float32, index)
     if cu_seqlens is not None:
-        _check("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev)
+        _expect("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index)
     out = {"d_xq": torch.empty_like(xq), "d_xk": torch.empty_like(xk), "d_xv": torch.empty_like(xv)}
     for name, w in (("d_conv_q", conv_q), ("d_conv_k", conv_k), ("d_conv_v", conv_v)):
         out[name] = torch.empty_like(w) if want_d_conv else None
     out["d_b_logit"], out["d_w_logit"] = torch.empty_like(b_logit), torch.empty_like(w_logit)
-    out["d_conv_state"] = torch.empty(st_shape, dtype=torch.float32, device=dev) if output_d_conv_state else None
+    out["d_conv_state"] = conv_q.new_empty(st_shape) if output_d_conv_state else None
     need = gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, K) if want_d_conv else 0
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    _run("gdn2_mixer_prologue_bwd", dev, xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), conv_q.data_ptr(),
+    workspace, ws_bytes = _workspace(workspace, need, xq.device)
+    _run("gdn2_mixer_prologue_bwd", index, xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), conv_q.data_ptr(),
          conv_k.data_ptr(), conv_v.data_ptr(), b_logit.data_ptr(), w_logit.data_ptr(), _addr(conv_state),
          d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), d_b.data_ptr(), d_w.data_ptr(), _addr(d_conv_state_out),
-         *(_addr(t) for t in out.values()), _addr(cu_seqlens), B, T, H, dk, dv, K, N, q_scale, eps_l2, code,
+         *[_addr(t) for t in out.values()], _addr(cu_seqlens), B, T, H, dk, dv, K, N, q_scale, eps_l2, code,
          _addr(workspace), ws_bytes)
     return out
