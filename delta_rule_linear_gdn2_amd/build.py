@@ -28,6 +28,7 @@ SOURCES = [
     "mixer.hip",
     "mixer_bwd.hip",
     "block.hip",
+    "block_bwd.hip",
     "colsum.hip",
     "scratch.hip",
     "segments.hip",

@@ -1,0 +1,312 @@
+// Gradients of the step from one block of a layer to the next (formulas:
+// block.hip), for gfx950.
+//
+// HBM-bound in its bytes (16 a bf16 element with a full gate), with about 65
+// vector instructions an element beside them, so what counts is wavefronts
+// enough to hide both.  A row is held in registers once: the stream's side (x',
+// dh, dx') is read first and makes t, and its registers take the next row's
+// loads while the block's side (u, gate) is worked on, and the other way round,
+// so the next row is always on its way without a second set of registers.  Two
+// sums over the row, one barrier each where it spans wavefronts.  The weights'
+// column sums stay in registers over all rows of a workgroup.
+#include "block_device.hpp"
+
+namespace gdn2 {
+namespace {
+
+// Wavefronts per SIMD that the register budget is set for: three (168 registers)
+// where a lane holds eight channels, two (256) at sixteen; sixteen wavefronts
+// are a workgroup of four a SIMD anyway.
+constexpr int bwd_waves_per_simd(int WPR, int NI) { return NI == 1 ? 3 : WPR == 16 ? 4 : 2; }
+
+// CHANNEL: the gate is one value per channel, whose gradient is a third column
+// sum (without it those registers are free).  FULL: D is a multiple of 8.
+template <typename T, typename R, int LPR, int WPR, int NI, bool FULL, bool CHANNEL>
+__global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_simd(WPR, NI))) void block_norm_bwd_kernel(BlockNormBwdArgs a)
+{
+    using C = Cover<LPR, WPR, NI>;
+    __shared__ float lds[2][16][4];
+    __shared__ float cols[C::kRows > 1 ? C::kWaves : 1][C::kRows > 1 ? 64 * 8 : 1];
+    int turn = 0;
+    const int slot = row_slot<LPR, WPR, NI>(), rl = threadIdx.x % C::kRowLanes;
+    const int64_t groups = (a.D + 7) / 8;
+    const uint64_t offset = a.drop.offset + (a.drop.offset_device ? *a.drop.offset_device : 0);
+    const bool has_u = a.u != nullptr, post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+    const bool has_dx = a.d_x_out != nullptr, full_gate = !CHANNEL && a.gate_layout == kGateFull,
+               token_gate = !CHANNEL && a.gate_layout == kGateToken;
+    const bool reads_u = has_u && (post || a.gate_layout != kGateNone);
+    const float inv_d = 1.0f / float(a.D);
+    const float factor = a.drop.threshold ? a.scale * a.drop.keep : a.scale;
+    uint32_t col[NI];
+    float wp[NI][8], wr[NI][8], ch[NI][8], acc_post[NI][8], acc_pre[NI][8], acc_gate[NI][8];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        col[i] = (i * C::kRowLanes + rl) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            wp[i][j] = wr[i][j] = ch[i][j] = 1.f;
+            acc_post[i][j] = acc_pre[i][j] = acc_gate[i][j] = 0.f;
+        }
+        if (post) load_weight(a.w_post, col[i], a.D, wp[i]);
+        if (pre) load_weight(a.w_pre, col[i], a.D, wr[i]);
+        if (CHANNEL) {
+            float g[8], df;
+            load_weight(static_cast<const float*>(a.gate), col[i], a.D, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) act_value(a.act, g[j], ch[i][j], df);
+        }
+    }
+    Eight<T> u[NI], g[NI], dh[NI];
+    Eight<R> x[NI], dx[NI];
+    float tok = 0.f;
+    auto load_stream = [&](int64_t row) {
+        const bool live = row < a.rows;
+        const int64_t at = row * a.D;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int n = live ? a.D - int(col[i]) : 0;
+            if (pre) {
+                x[i].template load<FULL>(static_cast<const R*>(a.x) + at + col[i], n);
+                dh[i].template load<FULL>(static_cast<const T*>(a.d_h) + at + col[i], n);
+            }
+            if (has_dx) dx[i].template load<FULL>(static_cast<const R*>(a.d_x_out) + at + col[i], n);
+        }
+    };
+    auto load_block = [&](int64_t row) {
+        const bool live = row < a.rows;
+        const int64_t at = row * a.D;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int n = live ? a.D - int(col[i]) : 0;
+            if (reads_u) u[i].template load<FULL>(static_cast<const T*>(a.u) + at + col[i], n);
+            if (full_gate) g[i].template load<FULL>(static_cast<const T*>(a.gate) + at + col[i], n);
+        }
+        if (token_gate) tok = live ? load_as_f32(static_cast<const T*>(a.gate), row) : 0.f;
+    };
+    const int64_t step = int64_t(gridDim.x) * C::kRows;
+    int64_t base = int64_t(blockIdx.x) * C::kRows;
+    load_stream(base + slot);
+    load_block(base + slot);
+    for (; base < a.rows; base += step) {
+        const int64_t row = base + slot;
+        const bool live = row < a.rows;
+
+        // t, the gradient of x'
+        float t[NI][8];
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (pre) {
+                float xv[8], hv[8];
+                x[i].get(xv);
+                dh[i].get(hv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    s[0] = fmaf(xv[j], xv[j], s[0]);
+                    s[1] = fmaf(wr[i][j] * hv[j], xv[j], s[1]);
+                }
+            }
+            if (post) {
+                float v[8];
+                u[i].get(v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[2] = fmaf(v[j], v[j], s[2]);
+            }
+        }
+        if (pre || post) row_sums<LPR, WPR, 3>(s, lds, turn);
+        const float rx = __builtin_amdgcn_rsqf(fmaf(s[0], inv_d, a.eps));
+        const float back_x = rx * rx * rx * s[1] * inv_d;
+        const float ru = post ? __builtin_amdgcn_rsqf(fmaf(s[2], inv_d, a.eps)) : 1.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (has_dx) {
+                dx[i].get(t[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[i][j] = 0.f;
+            }
+            if (pre) {
+                float xv[8], hv[8];
+                x[i].get(xv);
+                dh[i].get(hv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float hr = hv[j] * rx;
+                    acc_pre[i][j] = fmaf(hr, xv[j], acc_pre[i][j]);
+                    t[i][j] = fmaf(hr, wr[i][j], fmaf(-back_x, xv[j], t[i][j]));
+                }
+            }
+            Eight<R> out;
+            out.put(t[i]);
+            out.template store<FULL>(static_cast<R*>(a.d_x) + row * a.D + col[i], live ? a.D - int(col[i]) : 0);
+        }
+        if (base + step < a.rows) load_stream(row + step);
+        if (!has_u) continue;
+
+        float ta = 1.f, dta = 0.f;
+        if (token_gate) act_value(a.act, tok, ta, dta);
+        float q[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int n = live ? a.D - int(col[i]) : 0;
+            float uv[8], gv[8], dg[8];
+            if (reads_u) u[i].get(uv);
+            if (full_gate) g[i].get(gv);
+            u32x4_t bits{0, 0, 0, 0};
+            if (a.drop.threshold) bits = philox4x32(uint64_t(row * groups + col[i] / 8), offset, a.drop.seed);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                bool on = FULL ? n > 0 : j < n;  // not behind the row's end
+                if (a.drop.threshold) on = on && philox_keep(bits, j, a.drop.threshold);
+                const float c = on ? factor * t[i][j] : 0.f;
+                const float hat = reads_u ? uv[j] * ru : 0.f, nn = hat * wp[i][j];
+                float f = CHANNEL ? ch[i][j] : ta;
+                if (full_gate) {
+                    float df;
+                    act_value(a.act, gv[j], f, df);
+                    dg[j] = df * c * nn;
+                }
+                if (CHANNEL) acc_gate[i][j] = fmaf(c, nn, acc_gate[i][j]);
+                if (token_gate) q[1] = fmaf(c, nn, q[1]);
+                const float dn = c * f;
+                if (post) {
+                    acc_post[i][j] = fmaf(dn, hat, acc_post[i][j]);
+                    t[i][j] = wp[i][j] * dn;
+                    q[0] = fmaf(t[i][j], uv[j], q[0]);
+                } else {
+                    t[i][j] = dn;
+                }
+            }
+            if (full_gate && a.d_gate) {
+                Eight<T> out;
+                out.put(dg);
+                out.template store<FULL>(static_cast<T*>(a.d_gate) + row * a.D + col[i], n);
+            }
+        }
+        if (post || token_gate) row_sums<LPR, WPR, 2>(q, lds, turn);
+        if (token_gate && a.d_gate && rl == 0 && live) store_from_f32(static_cast<T*>(a.d_gate), row, dta * q[1]);
+        const float back_u = ru * ru * ru * q[0] * inv_d;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (post) {
+                float uv[8];
+                u[i].get(uv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[i][j] = fmaf(ru, t[i][j], -back_u * uv[j]);
+            }
+            Eight<T> out;
+            out.put(t[i]);
+            out.template store<FULL>(static_cast<T*>(a.d_u) + row * a.D + col[i], live ? a.D - int(col[i]) : 0);
+        }
+        if (base + step < a.rows) load_block(row + step);
+    }
+
+    // this workgroup's column sums into its partial row: over the row slots of
+    // a wavefront by lane exchanges, then over the wavefronts in LDS
+    const int sums = (a.d_w_post != nullptr) + (a.d_w_pre != nullptr) + (CHANNEL && a.d_gate);
+    int64_t at = int64_t(blockIdx.x) * sums * a.D;
+    auto put_sum = [&](float (&acc)[NI][8]) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (C::kRows > 1) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float v = acc[i][j];
+#pragma unroll
+                    for (int off = LPR; off < 64; off *= 2) v += __shfl_xor(v, off, 64);
+                    cols[threadIdx.x / 64][(threadIdx.x % 64) * 8 + j] = v;
+                }
+                __syncthreads();
+                if (slot == 0) {
+                    const int lane = threadIdx.x % 64;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float v = 0.f;
+                        for (int w = threadIdx.x / 64; w < C::kWaves; w += WPR) v += cols[w][lane * 8 + j];
+                        acc[i][j] = v;
+                    }
+                }
+                __syncthreads();
+            }
+            if (slot == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (int(col[i]) + j < a.D) a.partial[at + col[i] + j] = acc[i][j];
+            }
+        }
+        at += a.D;
+    };
+    if (a.d_w_post) put_sum(acc_post);
+    if (a.d_w_pre) put_sum(acc_pre);
+    if (CHANNEL && a.d_gate) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {  // act'(gate) is the column's own
+            float gv[8], f, df;
+            load_weight(static_cast<const float*>(a.gate), col[i], a.D, gv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                act_value(a.act, gv[j], f, df);
+                acc_gate[i][j] *= df;
+            }
+        }
+        put_sum(acc_gate);
+    }
+}
+
+template <typename T, typename R>
+hipError_t bwd_typed(const BlockNormBwdArgs& a, hipStream_t stream)
+{
+    const unsigned blocks = unsigned(block_bwd_partials(a.rows, a.D));
+    if (blocks > 0) {
+#define GDN2_LAUNCH(LPR, WPR, NI, FULL, CHANNEL)                                                             \
+    hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, LPR, WPR, NI, FULL, CHANNEL>), dim3(blocks),             \
+                       dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a)
+#define GDN2_BWD(LPR, WPR, NI)                                                                               \
+    do {                                                                                                     \
+        if (a.gate_layout == kGateChannel) {                                                                 \
+            if (a.D % 8 == 0) GDN2_LAUNCH(LPR, WPR, NI, true, true);                                         \
+            else GDN2_LAUNCH(LPR, WPR, NI, false, true);                                                     \
+        } else {                                                                                             \
+            if (a.D % 8 == 0) GDN2_LAUNCH(LPR, WPR, NI, true, false);                                        \
+            else GDN2_LAUNCH(LPR, WPR, NI, false, false);                                                    \
+        }                                                                                                    \
+    } while (0)
+        GDN2_COVER(a.D, GDN2_BWD);
+#undef GDN2_BWD
+#undef GDN2_LAUNCH
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    ColumnSumArgs c{};
+    c.partial = a.partial;
+    c.P = blocks;
+    int n = 0;
+    for (float* out : {a.d_w_post, a.d_w_pre, a.gate_layout == kGateChannel ? static_cast<float*>(a.d_gate) : nullptr})
+        if (out) {
+            c.out[n] = out;
+            c.width += a.D;
+            c.end[n++] = c.width;
+        }
+    for (; n < 3; ++n) c.end[n] = c.width;
+    return launch_column_sum(c, stream);
+}
+
+}  // namespace
+
+int64_t block_bwd_partials(int64_t rows, int32_t D)
+{
+    // as many workgroups as are resident at once on 256 compute units of four SIMDs
+    int waves = 1;
+#define GDN2_RESIDENT(LPR, WPR, NI) waves = bwd_waves_per_simd(WPR, NI)
+    GDN2_COVER(D, GDN2_RESIDENT);
+#undef GDN2_RESIDENT
+    return even_blocks(rows, rows_at_once(D), 256 * 4 * waves / workgroup_waves(D));
+}
+
+hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool bf16, bool residual_bf16, hipStream_t stream)
+{
+    if (!bf16) return bwd_typed<float, float>(a, stream);
+    return residual_bf16 ? bwd_typed<bf16raw, bf16raw>(a, stream) : bwd_typed<bf16raw, float>(a, stream);
+}
+
+}  // namespace gdn2

@@ -1,0 +1,122 @@
+// What the two directions of the block step (block.hip, block_bwd.hip) share: how
+// rows are laid over lanes and wavefronts, their sums, and the gate.
+#pragma once
+
+#include "row_device.hpp"
+
+namespace gdn2 {
+namespace {
+
+// A gate's activation and its derivative: 0 sigmoid s, 1 SiLU g s, 2 the value
+// itself.  Both derivatives are f (1 - s), plus s for SiLU.
+__device__ __forceinline__ void act_value(int act, float g, float& f, float& df)
+{
+    if (act == 2) {
+        f = g;
+        df = 1.f;
+        return;
+    }
+    const float s = fast_sigmoid(g);
+    f = act == 0 ? s : g * s;
+    df = fmaf(f, 1.f - s, act == 0 ? 0.f : s);
+}
+
+// How a workgroup covers rows: LPR lanes (LPR < 64) or WPR wavefronts a row, NI
+// groups of eight channels a lane.
+template <int LPR, int WPR, int NI>
+struct Cover {
+    static constexpr int kThreads = WPR <= 4 ? 256 : WPR * 64;
+    static constexpr int kWaves = kThreads / 64;
+    static constexpr int kRowLanes = LPR * WPR;
+    static constexpr int kRows = kThreads / kRowLanes;  // rows at a time per workgroup
+};
+
+// The row of this lane among those that the workgroup takes at a time: where a
+// row spans whole wavefronts, the same in every lane, which makes its address a
+// scalar.
+template <int LPR, int WPR, int NI>
+__device__ __forceinline__ int row_slot()
+{
+    const int slot = threadIdx.x / Cover<LPR, WPR, NI>::kRowLanes;
+    return LPR == 64 ? __builtin_amdgcn_readfirstlane(slot) : slot;
+}
+
+// Sums of M values over a row's lanes.  Over several wavefronts they meet in
+// LDS, in two buffers in turn: a wavefront that writes a buffer again has
+// passed the barrier that every reader of its last contents reached after
+// reading, so one barrier a sum is enough.
+template <int LPR, int WPR, int M>
+__device__ __forceinline__ void row_sums(float (&v)[M], float (*lds)[16][4], int& turn)
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = group_sum<LPR>(v[i]);
+    if (WPR == 1) return;
+    const int wave = threadIdx.x / 64, first = wave / WPR * WPR;
+    if (threadIdx.x % 64 == 0) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) lds[turn][wave][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < WPR; ++j) s += lds[turn][first + j][i];
+        v[i] = s;
+    }
+    turn ^= 1;
+}
+
+__device__ __forceinline__ void load_weight(const float* w, uint32_t col, int D, float* v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = int(col) + j < D ? w[col + j] : 0.f;
+}
+
+// The cover of a row of D channels: calls F(Cover parameters).  Narrow rows take
+// a group of lanes, then one wavefront, then as many as leave eight channels a
+// lane; the widest take sixteen a lane.
+#define GDN2_COVER(D, F)                     \
+    do {                                     \
+        if ((D) <= 32) F(4, 1, 1);           \
+        else if ((D) <= 64) F(8, 1, 1);      \
+        else if ((D) <= 128) F(16, 1, 1);    \
+        else if ((D) <= 256) F(32, 1, 1);    \
+        else if ((D) <= 512) F(64, 1, 1);    \
+        else if ((D) <= 1024) F(64, 2, 1);   \
+        else if ((D) <= 2048) F(64, 4, 1);   \
+        else if ((D) <= 4096) F(64, 8, 1);   \
+        else if ((D) <= 8192) F(64, 8, 2);   \
+        else F(64, 16, 2);                   \
+    } while (0)
+
+inline int rows_at_once(int32_t D)
+{
+    int n = 1;
+#define GDN2_ROWS(LPR, WPR, NI) n = Cover<LPR, WPR, NI>::kRows
+    GDN2_COVER(D, GDN2_ROWS);
+#undef GDN2_ROWS
+    return n;
+}
+
+inline int workgroup_waves(int32_t D)
+{
+    int n = 1;
+#define GDN2_WAVES(LPR, WPR, NI) n = Cover<LPR, WPR, NI>::kWaves
+    GDN2_COVER(D, GDN2_WAVES);
+#undef GDN2_WAVES
+    return n;
+}
+
+// Workgroups of a launch over `rows` rows that walk the same number of rounds of
+// `at_once` rows each, at most `most` of them.
+inline int64_t even_blocks(int64_t rows, int at_once, int64_t most)
+{
+    const int64_t need = (rows + at_once - 1) / at_once;
+    if (need <= most) return need;
+    const int64_t rounds = (need + most - 1) / most;
+    return (need + rounds - 1) / rounds;
+}
+
+}  // namespace
+}  // namespace gdn2

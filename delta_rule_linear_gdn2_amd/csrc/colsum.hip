@@ -2,21 +2,23 @@
 //
 // The kernels that produce weight gradients walk many rows each and leave one
 // partial row per workgroup (or run of tokens) in the workspace.  Here column c
-// is summed over the P partial rows in a fixed order: a workgroup takes 64
-// columns, its 16 wavefronts the partial rows 16 apart, and the 16 sums meet in
-// LDS.  No atomics, so results repeat bit for bit.
+// is summed over the P partial rows in a fixed order: a workgroup takes 16
+// columns (64 bytes a row, one memory segment), its 64 groups of 16 lanes the
+// partial rows 64 apart, and the 64 sums meet in LDS.  Narrow tiles, because
+// the columns are few: what bounds this is the length of a lane's chain of
+// loads.  No atomics, so results repeat bit for bit.
 #include "launch.hpp"
 
 namespace gdn2 {
 namespace {
 
-constexpr int kSlices = 16;
+constexpr int kCols = 16, kSlices = 64;
 
-__global__ __launch_bounds__(64 * kSlices) void column_sum_kernel(ColumnSumArgs a)
+__global__ __launch_bounds__(kCols * kSlices) void column_sum_kernel(ColumnSumArgs a)
 {
-    __shared__ float part[kSlices][64];
-    const int lane = threadIdx.x % 64, slice = threadIdx.x / 64;
-    const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+    __shared__ float part[kSlices][kCols + 1];
+    const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
+    const int64_t c = int64_t(blockIdx.x) * kCols + lane;
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
     if (c < a.width) {
         int64_t r = slice;
@@ -30,10 +32,13 @@ __global__ __launch_bounds__(64 * kSlices) void column_sum_kernel(ColumnSumArgs 
     }
     part[slice][lane] = (s0 + s1) + (s2 + s3);
     __syncthreads();
-    if (slice != 0 || c >= a.width) return;
+    if (slice >= 4) return;  // the first wavefront: four lanes a column
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSlices; ++i) s += part[i][lane];
+    for (int i = 0; i < kSlices / 4; ++i) s += part[slice * (kSlices / 4) + i][lane];
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (slice != 0 || c >= a.width) return;
     int64_t begin = 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
@@ -46,10 +51,10 @@ __global__ __launch_bounds__(64 * kSlices) void column_sum_kernel(ColumnSumArgs 
 
 hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream)
 {
-    const int64_t blocks = (a.width + 63) / 64;
+    const int64_t blocks = (a.width + kCols - 1) / kCols;
     if (blocks == 0) return hipSuccess;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(column_sum_kernel, dim3(unsigned(blocks)), dim3(64 * kSlices), 0, stream, a);
+    hipLaunchKernelGGL(column_sum_kernel, dim3(unsigned(blocks)), dim3(kCols * kSlices), 0, stream, a);
     return hipGetLastError();
 }
 
