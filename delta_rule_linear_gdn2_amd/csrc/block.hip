@@ -27,8 +27,7 @@
 namespace gdn2 {
 namespace {
 
-// FULL: D is a multiple of 8, so every group is whole and at a 16-byte boundary.
-template <typename T, typename R, int LPR, int WPR, int NI, bool FULL>
+template <typename T, typename R, int LPR, int WPR, int NI, int MODE>
 __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fwd_kernel(BlockNormArgs a)
 {
     using C = Cover<LPR, WPR, NI>;
@@ -39,20 +38,20 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
     const uint64_t offset = a.drop.offset + (a.drop.offset_device ? *a.drop.offset_device : 0);
     const bool has_u = a.u != nullptr, post = a.w_post != nullptr, pre = a.w_pre != nullptr;
     const float inv_d = 1.0f / float(a.D);
-    uint32_t col[NI];
-    float wp[NI][8], wr[NI][8], ch[NI][8];
+    const float factor = a.drop.threshold ? a.scale * a.drop.keep : a.scale;
+    Group<MODE> grp[NI];
+    float wp[NI][8], wr[NI][8];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        col[i] = (i * C::kRowLanes + rl) * 8;
+        grp[i].init((i * C::kRowLanes + rl) * 8, a.D);
+        load_weight<MODE>(a.w_post, grp[i], a.D, wp[i]);
+        load_weight<MODE>(a.w_pre, grp[i], a.D, wr[i]);
+        if (a.gate_layout == kGateChannel) {  // a second weight of the branch
+            float g[8], f[8], df[8];
+            load_weight<MODE>(static_cast<const float*>(a.gate), grp[i], a.D, g);
+            act_values(a.act, g, f, df);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) wp[i][j] = wr[i][j] = ch[i][j] = 1.f;
-        if (post) load_weight(a.w_post, col[i], a.D, wp[i]);
-        if (pre) load_weight(a.w_pre, col[i], a.D, wr[i]);
-        if (a.gate_layout == kGateChannel) {
-            float g[8], da;
-            load_weight(static_cast<const float*>(a.gate), col[i], a.D, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) act_value(a.act, g[j], ch[i][j], da);
+            for (int j = 0; j < 8; ++j) wp[i][j] *= f[j];
         }
     }
     Eight<T> nu[NI], ng[NI];
@@ -60,13 +59,12 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
     float nt = 0.f;
     auto load_row = [&](int64_t row) {
         const bool live = row < a.rows;
-        const int64_t at = row * a.D;
+        const int64_t at = (MODE != kRagged || live ? row : a.rows - 1) * a.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int n = live ? a.D - int(col[i]) : 0;
-            nx[i].template load<FULL>(static_cast<const R*>(a.x) + at + col[i], n);
-            if (has_u) nu[i].template load<FULL>(static_cast<const T*>(a.u) + at + col[i], n);
-            if (a.gate_layout == kGateFull) ng[i].template load<FULL>(static_cast<const T*>(a.gate) + at + col[i], n);
+            grp[i].load(nx[i], static_cast<const R*>(a.x) + at, a.D, live);
+            if (has_u) grp[i].load(nu[i], static_cast<const T*>(a.u) + at, a.D, live);
+            if (a.gate_layout == kGateFull) grp[i].load(ng[i], static_cast<const T*>(a.gate) + at, a.D, live);
         }
         if (a.gate_layout == kGateToken) nt = live ? load_as_f32(static_cast<const T*>(a.gate), row) : 0.f;
     };
@@ -84,6 +82,9 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
             u[i] = nu[i];
             g[i] = ng[i];
             x[i] = nx[i];
+            grp[i].settle(x[i], a.D, live);
+            if (has_u) grp[i].settle(u[i], a.D, live);
+            if (a.gate_layout == kGateFull) grp[i].settle(g[i], a.D, live);
         }
         if (base + step < a.rows) load_row(row + step);
 
@@ -100,37 +101,43 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
             row_sums<LPR, WPR, 1>(s, lds, turn);
             ru = __builtin_amdgcn_rsqf(fmaf(s[0], inv_d, a.eps));
         }
-        float ta = 1.f, unused;
-        if (a.gate_layout == kGateToken) act_value(a.act, tok, ta, unused);
+        if (a.gate_layout == kGateToken) {
+            float f[8], df[8], g8[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g8[j] = tok;
+            act_values(a.act, g8, f, df);
+            ru *= f[0];
+        }
         float s[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int n = live ? a.D - int(col[i]) : 0;
             float xv[8];
             x[i].get(xv);
             if (has_u) {
-                float uv[8], gv[8];
-                u[i].get(uv);
-                if (a.gate_layout == kGateFull) g[i].get(gv);
-                u32x4_t bits{0, 0, 0, 0};
-                if (a.drop.threshold) bits = philox4x32(uint64_t(row * groups + col[i] / 8), offset, a.drop.seed);
+                float z[8];
+                u[i].get(z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float z = uv[j] * ru * wp[i][j] * ch[i][j] * ta;
-                    if (a.gate_layout == kGateFull) {
-                        float f, df;
-                        act_value(a.act, gv[j], f, df);
-                        z *= f;
-                    }
-                    if (a.drop.threshold) z = philox_keep(bits, j, a.drop.threshold) ? z * a.drop.keep : 0.f;
-                    xv[j] = fmaf(a.scale, z, xv[j]);
+                for (int j = 0; j < 8; ++j) z[j] *= ru * wp[i][j];
+                if (a.gate_layout == kGateFull) {
+                    float gv[8], f[8], df[8];
+                    g[i].get(gv);
+                    act_values(a.act, gv, f, df);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] *= f[j];
                 }
+                if (a.drop.threshold) {
+                    const u32x4_t bits = philox4x32(uint64_t(row * groups + grp[i].col / 8), offset, a.drop.seed);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] = philox_keep(bits, j, a.drop.threshold) ? z[j] : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) xv[j] = fmaf(factor, z[j], xv[j]);
                 x[i].put(xv);
-                x[i].template store<FULL>(static_cast<R*>(a.x_out) + row * a.D + col[i], n);
+                grp[i].store(x[i], static_cast<R*>(a.x_out) + row * a.D, a.D, live);
                 x[i].get(xv);  // what is stored, rounded
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] += (FULL ? n > 0 : j < n) ? xv[j] * xv[j] : 0.f;
+            for (int j = 0; j < 8; ++j) s[0] += grp[i].has(j, a.D, live) ? xv[j] * xv[j] : 0.f;
         }
         if (pre) {
             row_sums<LPR, WPR, 1>(s, lds, turn);
@@ -143,7 +150,7 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
                 for (int j = 0; j < 8; ++j) v[j] = v[j] * rx * wr[i][j];
                 Eight<T> h;
                 h.put(v);
-                h.template store<FULL>(static_cast<T*>(a.h) + row * a.D + col[i], live ? a.D - int(col[i]) : 0);
+                grp[i].store(h, static_cast<T*>(a.h) + row * a.D, a.D, live);
             }
         }
     }
@@ -156,35 +163,36 @@ hipError_t fwd_typed(const BlockNormArgs& a, hipStream_t stream)
 {
     const unsigned blocks = unsigned(even_blocks(a.rows, rows_at_once(a.D), kFwdBlocks));
     if (blocks == 0) return hipSuccess;
-#define GDN2_FWD(LPR, WPR, NI)                                                                                     \
-    do {                                                                                                           \
-        if (a.D % 8 == 0)                                                                                          \
-            hipLaunchKernelGGL((block_norm_fwd_kernel<T, R, LPR, WPR, NI, true>), dim3(blocks),                    \
-                               dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a);                                 \
-        else                                                                                                       \
-            hipLaunchKernelGGL((block_norm_fwd_kernel<T, R, LPR, WPR, NI, false>), dim3(blocks),                   \
-                               dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a);                                 \
-    } while (0)
+#define GDN2_FWD(LPR, WPR, NI, MODE)                                                          \
+    hipLaunchKernelGGL((block_norm_fwd_kernel<T, R, LPR, WPR, NI, MODE>), dim3(blocks),       \
+                       dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a)
     GDN2_COVER(a.D, GDN2_FWD);
 #undef GDN2_FWD
     return hipGetLastError();
 }
 
 // Dropout alone: a lane takes one block of eight elements of a row.
-template <typename T, bool FULL>
+template <typename T, int MODE>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutCall a, int64_t groups)
 {
     const uint64_t offset = a.drop.offset + (a.drop.offset_device ? *a.drop.offset_device : 0);
     const int64_t total = a.rows * groups;
+    const int rest = int(a.D % 8);  // elements of a row's last, short group
     for (int64_t b = int64_t(blockIdx.x) * 256 + threadIdx.x; b < total; b += int64_t(gridDim.x) * 256) {
-        int64_t e = b * 8, n = 8;
-        if (!FULL) {
-            const int64_t row = b / groups, d = (b - row * groups) * 8;
-            e = row * a.D + d;
-            n = a.D - d < 8 ? a.D - d : 8;
-        }
+        const int64_t row = MODE == kWhole ? 0 : b / groups, d = (b - row * groups) * 8;
+        const int64_t e = row * a.D + d;
+        const bool whole = MODE == kWhole || d + 8 <= a.D;
+        const T* x = static_cast<const T*>(a.x) + e;
+        T* y = static_cast<T*>(a.y) + e;
         Eight<T> r;
-        r.template load<FULL>(static_cast<const T*>(a.x) + e, int(n));
+        if (MODE == kWhole) {
+            r.load(x, true);
+        } else if (MODE == kRagged) {
+            r.load_any(x - (whole ? 0 : 8 - rest));
+            if (!whole) r.shift(8 - rest);
+        } else {
+            r.load_pieces(x, rest);
+        }
         if (a.drop.threshold) {
             float v[8];
             r.get(v);
@@ -193,7 +201,9 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutCall a, int64_t gro
             for (int j = 0; j < 8; ++j) v[j] = philox_keep(bits, j, a.drop.threshold) ? v[j] * a.drop.keep : 0.f;
             r.put(v);
         }
-        r.template store<FULL>(static_cast<T*>(a.y) + e, int(n));
+        if (MODE == kWhole) r.store(y);
+        else if (whole) r.store_any(y);
+        else r.store_pieces(y, rest);
     }
 }
 
@@ -202,11 +212,12 @@ hipError_t dropout_typed(const DropoutCall& a, hipStream_t stream)
 {
     const int64_t groups = (a.D + 7) / 8, need = (a.rows * groups + 255) / 256;
     if (need == 0) return hipSuccess;
-    const unsigned blocks = unsigned(need < (1 << 20) ? need : (1 << 20));
-    if (a.D % 8 == 0)
-        hipLaunchKernelGGL((dropout_kernel<T, true>), dim3(blocks), dim3(256), 0, stream, a, groups);
-    else
-        hipLaunchKernelGGL((dropout_kernel<T, false>), dim3(blocks), dim3(256), 0, stream, a, groups);
+    const dim3 blocks(unsigned(need < (1 << 20) ? need : (1 << 20))), threads(256);
+    switch (row_mode(a.D)) {
+        case kWhole: hipLaunchKernelGGL((dropout_kernel<T, kWhole>), blocks, threads, 0, stream, a, groups); break;
+        case kRagged: hipLaunchKernelGGL((dropout_kernel<T, kRagged>), blocks, threads, 0, stream, a, groups); break;
+        default: hipLaunchKernelGGL((dropout_kernel<T, kTiny>), blocks, threads, 0, stream, a, groups);
+    }
     return hipGetLastError();
 }
 

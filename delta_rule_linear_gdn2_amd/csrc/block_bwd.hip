@@ -20,8 +20,8 @@ namespace {
 constexpr int bwd_waves_per_simd(int WPR, int NI) { return NI == 1 ? 3 : WPR == 16 ? 4 : 2; }
 
 // CHANNEL: the gate is one value per channel, whose gradient is a third column
-// sum (without it those registers are free).  FULL: D is a multiple of 8.
-template <typename T, typename R, int LPR, int WPR, int NI, bool FULL, bool CHANNEL>
+// sum (without it those registers are free).  MODE: how rows lie.
+template <typename T, typename R, int LPR, int WPR, int NI, int MODE, bool CHANNEL>
 __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_simd(WPR, NI))) void block_norm_bwd_kernel(BlockNormBwdArgs a)
 {
     using C = Cover<LPR, WPR, NI>;
@@ -37,23 +37,19 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
     const bool reads_u = has_u && (post || a.gate_layout != kGateNone);
     const float inv_d = 1.0f / float(a.D);
     const float factor = a.drop.threshold ? a.scale * a.drop.keep : a.scale;
-    uint32_t col[NI];
+    Group<MODE> grp[NI];
     float wp[NI][8], wr[NI][8], ch[NI][8], acc_post[NI][8], acc_pre[NI][8], acc_gate[NI][8];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        col[i] = (i * C::kRowLanes + rl) * 8;
+        grp[i].init((i * C::kRowLanes + rl) * 8, a.D);
+        load_weight<MODE>(a.w_post, grp[i], a.D, wp[i]);
+        load_weight<MODE>(a.w_pre, grp[i], a.D, wr[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            wp[i][j] = wr[i][j] = ch[i][j] = 1.f;
-            acc_post[i][j] = acc_pre[i][j] = acc_gate[i][j] = 0.f;
-        }
-        if (post) load_weight(a.w_post, col[i], a.D, wp[i]);
-        if (pre) load_weight(a.w_pre, col[i], a.D, wr[i]);
+        for (int j = 0; j < 8; ++j) acc_post[i][j] = acc_pre[i][j] = acc_gate[i][j] = 0.f;
         if (CHANNEL) {
-            float g[8], df;
-            load_weight(static_cast<const float*>(a.gate), col[i], a.D, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) act_value(a.act, g[j], ch[i][j], df);
+            float gv[8], df[8];
+            load_weight<MODE>(static_cast<const float*>(a.gate), grp[i], a.D, gv);
+            act_values(a.act, gv, ch[i], df);
         }
     }
     Eight<T> u[NI], g[NI], dh[NI];
@@ -61,25 +57,23 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
     float tok = 0.f;
     auto load_stream = [&](int64_t row) {
         const bool live = row < a.rows;
-        const int64_t at = row * a.D;
+        const int64_t at = (MODE != kRagged || live ? row : a.rows - 1) * a.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int n = live ? a.D - int(col[i]) : 0;
             if (pre) {
-                x[i].template load<FULL>(static_cast<const R*>(a.x) + at + col[i], n);
-                dh[i].template load<FULL>(static_cast<const T*>(a.d_h) + at + col[i], n);
+                grp[i].load(x[i], static_cast<const R*>(a.x) + at, a.D, live);
+                grp[i].load(dh[i], static_cast<const T*>(a.d_h) + at, a.D, live);
             }
-            if (has_dx) dx[i].template load<FULL>(static_cast<const R*>(a.d_x_out) + at + col[i], n);
+            if (has_dx) grp[i].load(dx[i], static_cast<const R*>(a.d_x_out) + at, a.D, live);
         }
     };
     auto load_block = [&](int64_t row) {
         const bool live = row < a.rows;
-        const int64_t at = row * a.D;
+        const int64_t at = (MODE != kRagged || live ? row : a.rows - 1) * a.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int n = live ? a.D - int(col[i]) : 0;
-            if (reads_u) u[i].template load<FULL>(static_cast<const T*>(a.u) + at + col[i], n);
-            if (full_gate) g[i].template load<FULL>(static_cast<const T*>(a.gate) + at + col[i], n);
+            if (reads_u) grp[i].load(u[i], static_cast<const T*>(a.u) + at, a.D, live);
+            if (full_gate) grp[i].load(g[i], static_cast<const T*>(a.gate) + at, a.D, live);
         }
         if (token_gate) tok = live ? load_as_f32(static_cast<const T*>(a.gate), row) : 0.f;
     };
@@ -98,6 +92,8 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
         for (int i = 0; i < NI; ++i) {
             if (pre) {
                 float xv[8], hv[8];
+                grp[i].settle(x[i], a.D, live);
+                grp[i].settle(dh[i], a.D, live);
                 x[i].get(xv);
                 dh[i].get(hv);
 #pragma unroll
@@ -106,6 +102,9 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
                     s[1] = fmaf(wr[i][j] * hv[j], xv[j], s[1]);
                 }
             }
+            if (has_dx) grp[i].settle(dx[i], a.D, live);
+            if (reads_u) grp[i].settle(u[i], a.D, live);
+            if (full_gate) grp[i].settle(g[i], a.D, live);
             if (post) {
                 float v[8];
                 u[i].get(v);
@@ -138,49 +137,68 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
             }
             Eight<R> out;
             out.put(t[i]);
-            out.template store<FULL>(static_cast<R*>(a.d_x) + row * a.D + col[i], live ? a.D - int(col[i]) : 0);
+            grp[i].store(out, static_cast<R*>(a.d_x) + row * a.D, a.D, live);
         }
         if (base + step < a.rows) load_stream(row + step);
         if (!has_u) continue;
 
         float ta = 1.f, dta = 0.f;
-        if (token_gate) act_value(a.act, tok, ta, dta);
+        if (token_gate) {
+            float g8[8], f[8], df[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g8[j] = tok;
+            act_values(a.act, g8, f, df);
+            ta = f[0];
+            dta = df[0];
+        }
         float q[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int n = live ? a.D - int(col[i]) : 0;
-            float uv[8], gv[8], dg[8];
-            if (reads_u) u[i].get(uv);
-            if (full_gate) g[i].get(gv);
-            u32x4_t bits{0, 0, 0, 0};
-            if (a.drop.threshold) bits = philox4x32(uint64_t(row * groups + col[i] / 8), offset, a.drop.seed);
+            // c = scale * m * t, nothing behind the row's end
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                bool on = FULL ? n > 0 : j < n;  // not behind the row's end
-                if (a.drop.threshold) on = on && philox_keep(bits, j, a.drop.threshold);
-                const float c = on ? factor * t[i][j] : 0.f;
-                const float hat = reads_u ? uv[j] * ru : 0.f, nn = hat * wp[i][j];
-                float f = CHANNEL ? ch[i][j] : ta;
-                if (full_gate) {
-                    float df;
-                    act_value(a.act, gv[j], f, df);
-                    dg[j] = df * c * nn;
+            for (int j = 0; j < 8; ++j) t[i][j] = grp[i].has(j, a.D, live) ? factor * t[i][j] : 0.f;
+            if (a.drop.threshold) {
+                const u32x4_t bits = philox4x32(uint64_t(row * groups + grp[i].col / 8), offset, a.drop.seed);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[i][j] = philox_keep(bits, j, a.drop.threshold) ? t[i][j] : 0.f;
+            }
+            float uv[8] = {}, hat[8];
+            if (reads_u) u[i].get(uv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) hat[j] = uv[j] * ru;
+            if (full_gate) {
+                float gv[8], f[8], df[8];
+                g[i].get(gv);
+                act_values(a.act, gv, f, df);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) df[j] *= t[i][j] * (hat[j] * wp[i][j]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[i][j] *= f[j];
+                if (a.d_gate) {
+                    Eight<T> out;
+                    out.put(df);
+                    grp[i].store(out, static_cast<T*>(a.d_gate) + row * a.D, a.D, live);
                 }
-                if (CHANNEL) acc_gate[i][j] = fmaf(c, nn, acc_gate[i][j]);
-                if (token_gate) q[1] = fmaf(c, nn, q[1]);
-                const float dn = c * f;
-                if (post) {
-                    acc_post[i][j] = fmaf(dn, hat, acc_post[i][j]);
-                    t[i][j] = wp[i][j] * dn;
-                    q[0] = fmaf(t[i][j], uv[j], q[0]);
-                } else {
-                    t[i][j] = dn;
+            } else if (CHANNEL) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc_gate[i][j] = fmaf(t[i][j], hat[j] * wp[i][j], acc_gate[i][j]);
+                    t[i][j] *= ch[i][j];
+                }
+            } else if (token_gate) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    q[1] = fmaf(t[i][j], hat[j] * wp[i][j], q[1]);
+                    t[i][j] *= ta;
                 }
             }
-            if (full_gate && a.d_gate) {
-                Eight<T> out;
-                out.put(dg);
-                out.template store<FULL>(static_cast<T*>(a.d_gate) + row * a.D + col[i], n);
+            if (post) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc_post[i][j] = fmaf(t[i][j], hat[j], acc_post[i][j]);
+                    t[i][j] *= wp[i][j];
+                    q[0] = fmaf(t[i][j], uv[j], q[0]);
+                }
             }
         }
         if (post || token_gate) row_sums<LPR, WPR, 2>(q, lds, turn);
@@ -196,7 +214,7 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
             }
             Eight<T> out;
             out.put(t[i]);
-            out.template store<FULL>(static_cast<T*>(a.d_u) + row * a.D + col[i], live ? a.D - int(col[i]) : 0);
+            grp[i].store(out, static_cast<T*>(a.d_u) + row * a.D, a.D, live);
         }
         if (base + step < a.rows) load_block(row + step);
     }
@@ -229,9 +247,9 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
                 __syncthreads();
             }
             if (slot == 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (int(col[i]) + j < a.D) a.partial[at + col[i] + j] = acc[i][j];
+                Eight<float> out;
+                out.put(acc[i]);
+                grp[i].store(out, a.partial + at, a.D, true);
             }
         }
         at += a.D;
@@ -241,13 +259,11 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
     if (CHANNEL && a.d_gate) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {  // act'(gate) is the column's own
-            float gv[8], f, df;
-            load_weight(static_cast<const float*>(a.gate), col[i], a.D, gv);
+            float gv[8], f[8], df[8];
+            load_weight<MODE>(static_cast<const float*>(a.gate), grp[i], a.D, gv);
+            act_values(a.act, gv, f, df);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                act_value(a.act, gv[j], f, df);
-                acc_gate[i][j] *= df;
-            }
+            for (int j = 0; j < 8; ++j) acc_gate[i][j] *= df[j];
         }
         put_sum(acc_gate);
     }
@@ -258,22 +274,17 @@ hipError_t bwd_typed(const BlockNormBwdArgs& a, hipStream_t stream)
 {
     const unsigned blocks = unsigned(block_bwd_partials(a.rows, a.D));
     if (blocks > 0) {
-#define GDN2_LAUNCH(LPR, WPR, NI, FULL, CHANNEL)                                                             \
-    hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, LPR, WPR, NI, FULL, CHANNEL>), dim3(blocks),             \
-                       dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a)
-#define GDN2_BWD(LPR, WPR, NI)                                                                               \
-    do {                                                                                                     \
-        if (a.gate_layout == kGateChannel) {                                                                 \
-            if (a.D % 8 == 0) GDN2_LAUNCH(LPR, WPR, NI, true, true);                                         \
-            else GDN2_LAUNCH(LPR, WPR, NI, false, true);                                                     \
-        } else {                                                                                             \
-            if (a.D % 8 == 0) GDN2_LAUNCH(LPR, WPR, NI, true, false);                                        \
-            else GDN2_LAUNCH(LPR, WPR, NI, false, false);                                                    \
-        }                                                                                                    \
+#define GDN2_BWD(LPR, WPR, NI, MODE)                                                                      \
+    do {                                                                                                  \
+        if (a.gate_layout == kGateChannel)                                                                \
+            hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, LPR, WPR, NI, MODE, true>), dim3(blocks),     \
+                               dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a);                        \
+        else                                                                                              \
+            hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, LPR, WPR, NI, MODE, false>), dim3(blocks),    \
+                               dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a);                        \
     } while (0)
         GDN2_COVER(a.D, GDN2_BWD);
 #undef GDN2_BWD
-#undef GDN2_LAUNCH
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -297,7 +308,7 @@ int64_t block_bwd_partials(int64_t rows, int32_t D)
 {
     // as many workgroups as are resident at once on 256 compute units of four SIMDs
     int waves = 1;
-#define GDN2_RESIDENT(LPR, WPR, NI) waves = bwd_waves_per_simd(WPR, NI)
+#define GDN2_RESIDENT(LPR, WPR, NI, MODE) waves = bwd_waves_per_simd(WPR, NI)
     GDN2_COVER(D, GDN2_RESIDENT);
 #undef GDN2_RESIDENT
     return even_blocks(rows, rows_at_once(D), 256 * 4 * waves / workgroup_waves(D));

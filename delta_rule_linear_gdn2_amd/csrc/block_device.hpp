@@ -7,18 +7,35 @@
 namespace gdn2 {
 namespace {
 
-// A gate's activation and its derivative: 0 sigmoid s, 1 SiLU g s, 2 the value
-// itself.  Both derivatives are f (1 - s), plus s for SiLU.
-__device__ __forceinline__ void act_value(int act, float g, float& f, float& df)
+// Conditions that are the same for a whole launch (norms, gate, dropout) are
+// asked once per group of eight channels, with a loop over the eight inside:
+// asked per element they cost a scalar branch each and keep the compiler from
+// interleaving the eight chains.
+
+// A gate's activation and its derivative over eight channels: 0 sigmoid s, 1
+// SiLU g s, 2 the value itself.  Both derivatives are f (1 - s), plus s for SiLU.
+__device__ __forceinline__ void act_values(int act, const float* g, float* f, float* df)
 {
     if (act == 2) {
-        f = g;
-        df = 1.f;
-        return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = g[j];
+            df[j] = 1.f;
+        }
+    } else if (act == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = fast_sigmoid(g[j]);
+            f[j] = g[j] * s;
+            df[j] = fmaf(f[j], 1.f - s, s);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = fast_sigmoid(g[j]);
+            df[j] = f[j] * (1.f - f[j]);
+        }
     }
-    const float s = fast_sigmoid(g);
-    f = act == 0 ? s : g * s;
-    df = fmaf(f, 1.f - s, act == 0 ? 0.f : s);
 }
 
 // How a workgroup covers rows: LPR lanes (LPR < 64) or WPR wavefronts a row, NI
@@ -67,33 +84,48 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float (*lds)[16][4], int
     turn ^= 1;
 }
 
-__device__ __forceinline__ void load_weight(const float* w, uint32_t col, int D, float* v)
+// Eight channels of a weight (zero behind the last), or ones without it.
+template <int MODE>
+__device__ __forceinline__ void load_weight(const float* w, const Group<MODE>& group, int D, float* v)
 {
+    if (!w) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = int(col) + j < D ? w[col + j] : 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = 1.f;
+        return;
+    }
+    Eight<float> e;
+    group.load(e, w, D, true);
+    group.settle(e, D, true);
+    e.get(v);
 }
 
-// The cover of a row of D channels: calls F(Cover parameters).  Narrow rows take
+// The cover of a row of D channels: calls F(Cover parameters, MODE).  Narrow rows take
 // a group of lanes, then one wavefront, then as many as leave eight channels a
 // lane; the widest take sixteen a lane.
-#define GDN2_COVER(D, F)                     \
-    do {                                     \
-        if ((D) <= 32) F(4, 1, 1);           \
-        else if ((D) <= 64) F(8, 1, 1);      \
-        else if ((D) <= 128) F(16, 1, 1);    \
-        else if ((D) <= 256) F(32, 1, 1);    \
-        else if ((D) <= 512) F(64, 1, 1);    \
-        else if ((D) <= 1024) F(64, 2, 1);   \
-        else if ((D) <= 2048) F(64, 4, 1);   \
-        else if ((D) <= 4096) F(64, 8, 1);   \
-        else if ((D) <= 8192) F(64, 8, 2);   \
-        else F(64, 16, 2);                   \
+#define GDN2_COVER(D, F)                            \
+    do {                                            \
+        if (row_mode(D) == kTiny) F(4, 1, 1, kTiny); \
+        else if (row_mode(D) == kWhole) GDN2_WIDTH(D, F, kWhole);  \
+        else GDN2_WIDTH(D, F, kRagged);             \
+    } while (0)
+#define GDN2_WIDTH(D, F, MODE)                     \
+    do {                                           \
+        if ((D) <= 32) F(4, 1, 1, MODE);           \
+        else if ((D) <= 64) F(8, 1, 1, MODE);      \
+        else if ((D) <= 128) F(16, 1, 1, MODE);    \
+        else if ((D) <= 256) F(32, 1, 1, MODE);    \
+        else if ((D) <= 512) F(64, 1, 1, MODE);    \
+        else if ((D) <= 1024) F(64, 2, 1, MODE);   \
+        else if ((D) <= 2048) F(64, 4, 1, MODE);   \
+        else if ((D) <= 4096) F(64, 4, 2, MODE);   \
+        else if ((D) <= 8192) F(64, 8, 2, MODE);   \
+        else F(64, 16, 2, MODE);                   \
     } while (0)
 
 inline int rows_at_once(int32_t D)
 {
     int n = 1;
-#define GDN2_ROWS(LPR, WPR, NI) n = Cover<LPR, WPR, NI>::kRows
+#define GDN2_ROWS(LPR, WPR, NI, MODE) n = Cover<LPR, WPR, NI>::kRows
     GDN2_COVER(D, GDN2_ROWS);
 #undef GDN2_ROWS
     return n;
@@ -102,7 +134,7 @@ inline int rows_at_once(int32_t D)
 inline int workgroup_waves(int32_t D)
 {
     int n = 1;
-#define GDN2_WAVES(LPR, WPR, NI) n = Cover<LPR, WPR, NI>::kWaves
+#define GDN2_WAVES(LPR, WPR, NI, MODE) n = Cover<LPR, WPR, NI>::kWaves
     GDN2_COVER(D, GDN2_WAVES);
 #undef GDN2_WAVES
     return n;

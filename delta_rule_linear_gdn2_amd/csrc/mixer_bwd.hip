@@ -51,12 +51,12 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
     }
     for (int64_t base = int64_t(blockIdx.x) * RPB; base < a.rows; base += int64_t(gridDim.x) * RPB) {
         const int64_t r = base + wave * RPW + lane / G;
-        const int n = r < a.rows ? 8 : 0;
+        const bool on = r < a.rows;
         const int64_t e = r * DV + c0;
         Eight<T> ro, rg, ry;
-        ro.template load<true>(static_cast<const T*>(a.o) + e, n);
-        rg.template load<true>(static_cast<const T*>(a.gate) + e, n);
-        ry.template load<true>(static_cast<const T*>(a.d_y) + e, n);
+        ro.load(static_cast<const T*>(a.o) + e, on);
+        rg.load(static_cast<const T*>(a.gate) + e, on);
+        ry.load(static_cast<const T*>(a.d_y) + e, on);
         float o[8], g[8], y[8], dn[8], dg[8];
         ro.get(o);
         rg.get(g);
@@ -85,9 +85,9 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
         }
         Eight<T> out;
         out.put(d);
-        out.template store<true, true>(static_cast<T*>(a.d_o) + e, n);
+        if (on) out.template store<true>(static_cast<T*>(a.d_o) + e);
         out.put(dg);
-        out.template store<true, true>(static_cast<T*>(a.d_gate) + e, n);
+        if (on) out.template store<true>(static_cast<T*>(a.d_gate) + e);
     }
     if (!a.d_weight) return;
 #pragma unroll
@@ -469,8 +469,8 @@ __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t 
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const int64_t at = (t + i < t1 ? t + i : t1 - 1) * stride;
-            rl[i].template load<true>(logit + at + chan, 8);
-            rd[i].template load<true>(dg + at + chan, 8);
+            rl[i].load(logit + at + chan, true);
+            rd[i].load(dg + at + chan, true);
         }
 #pragma unroll
         for (int i = 0; i < M; ++i) {
@@ -484,7 +484,7 @@ __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t 
                 d[j] *= s * (1.f - s);
             }
             rd[i].put(d);
-            rd[i].template store<true, true>(out + (t + i) * stride + chan, 8);
+            rd[i].template store<true>(out + (t + i) * stride + chan);
         }
     }
 }

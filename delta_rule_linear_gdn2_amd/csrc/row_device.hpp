@@ -40,18 +40,28 @@ __device__ __forceinline__ float group_sum(float x)
 // It keeps its limits: 0 and 1 at minus and plus infinity, NaN for NaN.
 __device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
+// Eight consecutive elements of a row as loaded (bf16 stays packed until used).
+//
+// Where the row length is a multiple of eight, each group is whole and at a
+// 16-byte boundary and loaded as it is.  In ragged rows a
+// group sits at any element boundary, which gfx950 takes for 16-byte accesses,
+// and the last one is short.  That one is loaded whole all the same, from the
+// row's last eight elements, and shifted into place when it is used: taken in
+// pieces, it would be waited for where it is loaded, and with it everything
+// loaded before.  It is stored in pieces of four, two and one.  Rows of under
+// eight elements are loaded in such pieces too.
+//
 // STREAM in a store: past the caches, for outputs that no cache will hold until
 // they are read.
-//
-// Eight consecutive elements of a row as loaded (bf16 stays packed until used).
-// FULL: the eight exist and sit at a 16-byte boundary.  Otherwise n of them
-// exist (n <= 0: none) and the address is aligned to the element only: gfx950
-// takes 16-byte accesses at any element boundary, and the last group of a row
-// goes element by element.
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef u32x2_t u32x2_any __attribute__((aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
 typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+typedef f32x2_t f32x2_any __attribute__((aligned(4)));
 
 template <bool STREAM, typename V, typename P>
 __device__ __forceinline__ void put16(P* p, const V& v)
@@ -66,22 +76,43 @@ struct Eight;
 template <>
 struct Eight<bf16raw> {
     u32x4_t u;
-    template <bool FULL>
-    __device__ __forceinline__ void load(const bf16raw* p, int n)
+    // A whole group at a 16-byte boundary, or zeros.
+    __device__ __forceinline__ void load(const bf16raw* p, bool on)
     {
-        if (FULL) {
-            if (n > 0) u = *reinterpret_cast<const u32x4_t*>(p);
-            else u = u32x4_t{0, 0, 0, 0};
-            return;
+        if (on) u = *reinterpret_cast<const u32x4_t*>(p);
+        else u = u32x4_t{0, 0, 0, 0};
+    }
+    // A whole group at any boundary.
+    __device__ __forceinline__ void load_any(const bf16raw* p) { u = *reinterpret_cast<const u32x4_any*>(p); }
+    // The first n < 8 elements, zeros behind them.
+    __device__ __forceinline__ void load_pieces(const bf16raw* p, int n)
+    {
+        u = u32x4_t{0, 0, 0, 0};
+        if (n <= 0) return;
+        if (n & 4) {
+            const u32x2_any v = *reinterpret_cast<const u32x2_any*>(p);
+            u[0] = v[0];
+            u[1] = v[1];
         }
-        if (n >= 8) {
-            u = *reinterpret_cast<const u32x4_any*>(p);
-        } else {
-            uint32_t e[8];
+        if (n & 2) {
+            const uint32_t v = *reinterpret_cast<const u32_any*>(p + (n & 4));
+            if (n & 4) u[2] = v;
+            else u[0] = v;
+        }
+        if (n & 1) {
+            const uint32_t v = p[n & 6];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = j < n ? p[j] : 0u;
-            u = u32x4_t{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+            for (int j = 0; j < 4; ++j) u[j] = (n & 6) == 2 * j ? v : u[j];
         }
+    }
+    __device__ __forceinline__ void clear() { u = u32x4_t{0, 0, 0, 0}; }
+    // by < 8 elements down, zeros behind them.
+    __device__ __forceinline__ void shift(int by)
+    {
+        if (by & 4) u = u32x4_t{u[2], u[3], 0, 0};
+        if (by & 2) u = u32x4_t{u[1], u[2], u[3], 0};
+        if (by & 1)
+            u = u32x4_t{u[0] >> 16 | u[1] << 16, u[1] >> 16 | u[2] << 16, u[2] >> 16 | u[3] << 16, u[3] >> 16};
     }
     __device__ __forceinline__ void get(float* v) const
     {
@@ -96,47 +127,75 @@ struct Eight<bf16raw> {
         u = u32x4_t{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
                     f32x2_to_bf16x2(v[6], v[7])};
     }
-    template <bool FULL, bool STREAM = false>
-    __device__ __forceinline__ void store(bf16raw* p, int n) const
+    template <bool STREAM = false>
+    __device__ __forceinline__ void store(bf16raw* p) const
     {
-        if (FULL) {
-            if (n > 0) put16<STREAM>(p, u);
-            return;
-        }
-        if (n >= 8) {
-            *reinterpret_cast<u32x4_any*>(p) = u;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) p[j] = bf16raw(j & 1 ? u[j / 2] >> 16 : u[j / 2] & 0xffffu);
-        }
+        put16<STREAM>(p, u);
+    }
+    __device__ __forceinline__ void store_any(bf16raw* p) const { *reinterpret_cast<u32x4_any*>(p) = u; }
+    // The first n < 8 elements.
+    __device__ __forceinline__ void store_pieces(bf16raw* p, int n) const
+    {
+        if (n & 4) *reinterpret_cast<u32x2_any*>(p) = u32x2_t{u[0], u[1]};
+        if (n & 2) *reinterpret_cast<u32_any*>(p + (n & 4)) = n & 4 ? u[2] : u[0];
+        if (n & 1) p[n & 6] = bf16raw((n & 4 ? (n & 2 ? u[3] : u[2]) : (n & 2 ? u[1] : u[0])) & 0xffffu);
     }
 };
 
 template <>
 struct Eight<float> {
     f32x4_t a, b;
-    template <bool FULL>
-    __device__ __forceinline__ void load(const float* p, int n)
+    __device__ __forceinline__ void load(const float* p, bool on)
     {
-        if (FULL) {
-            if (n > 0) {
-                a = *reinterpret_cast<const f32x4_t*>(p);
-                b = *reinterpret_cast<const f32x4_t*>(p + 4);
-            } else {
-                a = b = f32x4_t{0, 0, 0, 0};
-            }
-            return;
-        }
-        if (n >= 8) {
-            a = *reinterpret_cast<const f32x4_any*>(p);
-            b = *reinterpret_cast<const f32x4_any*>(p + 4);
+        if (on) {
+            a = *reinterpret_cast<const f32x4_t*>(p);
+            b = *reinterpret_cast<const f32x4_t*>(p + 4);
         } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                a[j] = j < n ? p[j] : 0.f;
-                b[j] = j + 4 < n ? p[j + 4] : 0.f;
+            a = b = f32x4_t{0, 0, 0, 0};
+        }
+    }
+    __device__ __forceinline__ void load_any(const float* p)
+    {
+        a = *reinterpret_cast<const f32x4_any*>(p);
+        b = *reinterpret_cast<const f32x4_any*>(p + 4);
+    }
+    __device__ __forceinline__ void load_pieces(const float* p, int n)
+    {
+        a = b = f32x4_t{0, 0, 0, 0};
+        if (n <= 0) return;
+        if (n & 4) a = *reinterpret_cast<const f32x4_any*>(p);
+        if (n & 2) {
+            const f32x2_any v = *reinterpret_cast<const f32x2_any*>(p + (n & 4));
+            if (n & 4) {
+                b[0] = v[0];
+                b[1] = v[1];
+            } else {
+                a[0] = v[0];
+                a[1] = v[1];
             }
+        }
+        if (n & 1) {
+            const float v = p[n & 6];
+            a[0] = (n & 6) == 0 ? v : a[0];
+            a[2] = (n & 6) == 2 ? v : a[2];
+            b[0] = (n & 6) == 4 ? v : b[0];
+            b[2] = (n & 6) == 6 ? v : b[2];
+        }
+    }
+    __device__ __forceinline__ void clear() { a = b = f32x4_t{0, 0, 0, 0}; }
+    __device__ __forceinline__ void shift(int by)
+    {
+        if (by & 4) {
+            a = b;
+            b = f32x4_t{0, 0, 0, 0};
+        }
+        if (by & 2) {
+            a = f32x4_t{a[2], a[3], b[0], b[1]};
+            b = f32x4_t{b[2], b[3], 0, 0};
+        }
+        if (by & 1) {
+            a = f32x4_t{a[1], a[2], a[3], b[0]};
+            b = f32x4_t{b[1], b[2], b[3], 0};
         }
     }
     __device__ __forceinline__ void get(float* v) const
@@ -155,24 +214,77 @@ struct Eight<float> {
             b[j] = v[4 + j];
         }
     }
-    template <bool FULL, bool STREAM = false>
-    __device__ __forceinline__ void store(float* p, int n) const
+    template <bool STREAM = false>
+    __device__ __forceinline__ void store(float* p) const
     {
-        if (FULL) {
-            if (n > 0) {
-                put16<STREAM>(p, a);
-                put16<STREAM>(p + 4, b);
-            }
-            return;
+        put16<STREAM>(p, a);
+        put16<STREAM>(p + 4, b);
+    }
+    __device__ __forceinline__ void store_any(float* p) const
+    {
+        *reinterpret_cast<f32x4_any*>(p) = a;
+        *reinterpret_cast<f32x4_any*>(p + 4) = b;
+    }
+    __device__ __forceinline__ void store_pieces(float* p, int n) const
+    {
+        if (n & 4) *reinterpret_cast<f32x4_any*>(p) = a;
+        if (n & 2) *reinterpret_cast<f32x2_any*>(p + (n & 4)) = n & 4 ? f32x2_t{b[0], b[1]} : f32x2_t{a[0], a[1]};
+        if (n & 1) p[n & 6] = n & 4 ? (n & 2 ? b[2] : b[0]) : (n & 2 ? a[2] : a[0]);
+    }
+};
+
+// How the rows of a call lie, a template argument (MODE) of the kernels: whole
+// groups at 16-byte boundaries (D a multiple of eight), ragged rows, or rows of
+// under eight elements.  The last are apart because their loads in pieces, in
+// the same loop, would make the compiler wait before every other load.
+constexpr int kWhole = 0, kRagged = 1, kTiny = 2;
+inline int row_mode(int64_t D) { return D % 8 == 0 ? kWhole : D > 8 ? kRagged : kTiny; }
+
+// A lane's group of eight of a row of D elements.  In a ragged row it is whole,
+// short (the row's last D % 8 elements) or behind the row.  How short, and so how
+// far its load is shifted and which pieces are stored, is the same for every
+// row and lane, which makes those branches scalar.
+template <int MODE>
+struct Group {
+    uint32_t col, from;  // its first column, and where it is loaded
+    int kind;            // 0 whole, 1 short, 2 behind the row
+    __device__ __forceinline__ void init(uint32_t first, uint32_t D)
+    {
+        col = from = first;
+        kind = first >= D ? 2 : MODE == kWhole || first + 8 <= D ? 0 : 1;
+        if (MODE == kRagged && kind != 0) from = D - 8;
+    }
+    // The elements from row[0 .. D).  `on`: the row exists; a ragged row that does
+    // not is loaded nevertheless, from one that does, and settle() clears it.
+    template <typename T>
+    __device__ __forceinline__ void load(Eight<T>& e, const T* row, uint32_t D, bool on) const
+    {
+        if (MODE == kWhole) e.load(row + col, on && kind == 0);
+        else if (MODE == kRagged) e.load_any(row + from);
+        else e.load_pieces(row + col, on ? int(D) - int(col) : 0);
+    }
+    template <typename T>
+    __device__ __forceinline__ void settle(Eight<T>& e, uint32_t D, bool on) const
+    {
+        if (MODE != kRagged) return;
+        if (kind == 1) e.shift(8 - int(D % 8));
+        if (kind == 2 || !on) e.clear();
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(const Eight<T>& e, T* row, uint32_t D, bool on) const
+    {
+        if (!on) return;
+        if (kind == 0) {
+            if (MODE == kWhole) e.store(row + col);
+            else e.store_any(row + col);
+        } else if (MODE != kWhole && kind == 1) {
+            e.store_pieces(row + col, int(D % 8));
         }
-        if (n >= 8) {
-            *reinterpret_cast<f32x4_any*>(p) = a;
-            *reinterpret_cast<f32x4_any*>(p + 4) = b;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) p[j] = j < 4 ? a[j & 3] : b[j & 3];
-        }
+    }
+    // Whether element j of the group exists.
+    __device__ __forceinline__ bool has(int j, uint32_t D, bool on) const
+    {
+        return on && (MODE == kWhole ? kind == 0 : col + j < D);
     }
 };
 
