@@ -27,8 +27,15 @@
 namespace gdn2 {
 namespace {
 
+// Wavefronts per SIMD that the register budget is set for, and a launch's
+// workgroups with it.
+constexpr int fwd_waves_per_simd(int WPR, int NI, int MODE)
+{
+    return NI == 1 ? (MODE == kWhole ? 5 : 4) : WPR == 4 ? 3 : WPR == 8 ? 2 : 4;
+}
+
 template <typename T, typename R, int LPR, int WPR, int NI, int MODE>
-__global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fwd_kernel(BlockNormArgs a)
+__global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (fwd_waves_per_simd(WPR, NI, MODE))) void block_norm_fwd_kernel(BlockNormArgs a)
 {
     using C = Cover<LPR, WPR, NI>;
     __shared__ float lds[2][16][4];
@@ -54,39 +61,46 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
             for (int j = 0; j < 8; ++j) wp[i][j] *= f[j];
         }
     }
+    // The next row's loads: at the start of a row, into registers of their own,
+    // or, with five wavefronts a SIMD, when this row's x' is made, into the
+    // registers that it frees.
+    constexpr bool kEarly = MODE != kWhole || NI > 1;
     Eight<T> nu[NI], ng[NI];
     Eight<R> nx[NI];
-    float nt = 0.f;
+    float ntok = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        nu[i].clear();
+        ng[i].clear();
+        nx[i].clear();
+    }
     auto load_row = [&](int64_t row) {
-        const bool live = row < a.rows;
-        const int64_t at = (MODE != kRagged || live ? row : a.rows - 1) * a.D;
+        const bool live = row < a.rows, last = row >= a.rows - 1;
+        const int64_t at = row * a.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            grp[i].load(nx[i], static_cast<const R*>(a.x) + at, a.D, live);
-            if (has_u) grp[i].load(nu[i], static_cast<const T*>(a.u) + at, a.D, live);
-            if (a.gate_layout == kGateFull) grp[i].load(ng[i], static_cast<const T*>(a.gate) + at, a.D, live);
+            if (has_u) grp[i].load(nu[i], static_cast<const T*>(a.u) + at, a.D, live, last);
+            if (a.gate_layout == kGateFull) grp[i].load(ng[i], static_cast<const T*>(a.gate) + at, a.D, live, last);
+            grp[i].load(nx[i], static_cast<const R*>(a.x) + at, a.D, live, last);
         }
-        if (a.gate_layout == kGateToken) nt = live ? load_as_f32(static_cast<const T*>(a.gate), row) : 0.f;
+        if (a.gate_layout == kGateToken) ntok = live ? load_as_f32(static_cast<const T*>(a.gate), row) : 0.f;
     };
     const int64_t step = int64_t(gridDim.x) * C::kRows;
     int64_t base = int64_t(blockIdx.x) * C::kRows;
     load_row(base + slot);
     for (; base < a.rows; base += step) {
         const int64_t row = base + slot;
-        const bool live = row < a.rows;
+        const bool live = row < a.rows, last = row >= a.rows - 1;
         Eight<T> u[NI], g[NI];
         Eight<R> x[NI];
-        const float tok = nt;
+        const float tok = ntok;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             u[i] = nu[i];
             g[i] = ng[i];
             x[i] = nx[i];
-            grp[i].settle(x[i], a.D, live);
-            if (has_u) grp[i].settle(u[i], a.D, live);
-            if (a.gate_layout == kGateFull) grp[i].settle(g[i], a.D, live);
         }
-        if (base + step < a.rows) load_row(row + step);
+        if (kEarly && base + step < a.rows) load_row(row + step);
 
         float ru = 1.f;
         if (post) {
@@ -94,6 +108,7 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 float v[8];
+                grp[i].settle(u[i], a.D, last);
                 u[i].get(v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[0] = fmaf(v[j], v[j], s[0]);
@@ -109,17 +124,22 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
             ru *= f[0];
         }
         float s[1] = {0.f};
+        Eight<R> xo[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             float xv[8];
+            grp[i].settle(x[i], a.D, last);
+            xo[i] = x[i];
             x[i].get(xv);
             if (has_u) {
                 float z[8];
+                if (!post) grp[i].settle(u[i], a.D, last);
                 u[i].get(z);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) z[j] *= ru * wp[i][j];
                 if (a.gate_layout == kGateFull) {
                     float gv[8], f[8], df[8];
+                    grp[i].settle(g[i], a.D, last);
                     g[i].get(gv);
                     act_values(a.act, gv, f, df);
 #pragma unroll
@@ -132,20 +152,21 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) xv[j] = fmaf(factor, z[j], xv[j]);
-                x[i].put(xv);
-                grp[i].store(x[i], static_cast<R*>(a.x_out) + row * a.D, a.D, live);
-                x[i].get(xv);  // what is stored, rounded
+                xo[i].put(xv);
+                grp[i].store(xo[i], static_cast<R*>(a.x_out) + row * a.D, a.D, live);
+                xo[i].get(xv);  // what is stored, rounded
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] += grp[i].has(j, a.D, live) ? xv[j] * xv[j] : 0.f;
         }
+        if (!kEarly && base + step < a.rows) load_row(row + step);
         if (pre) {
             row_sums<LPR, WPR, 1>(s, lds, turn);
             const float rx = __builtin_amdgcn_rsqf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 float v[8];
-                x[i].get(v);
+                xo[i].get(v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = v[j] * rx * wr[i][j];
                 Eight<T> h;
@@ -156,12 +177,14 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads)) void block_norm_fw
     }
 }
 
-constexpr int64_t kFwdBlocks = 2048;
-
 template <typename T, typename R>
 hipError_t fwd_typed(const BlockNormArgs& a, hipStream_t stream)
 {
-    const unsigned blocks = unsigned(even_blocks(a.rows, rows_at_once(a.D), kFwdBlocks));
+    int waves = 1;
+#define GDN2_RESIDENT(LPR, WPR, NI, MODE) waves = fwd_waves_per_simd(WPR, NI, MODE)
+    GDN2_COVER(a.D, GDN2_RESIDENT);
+#undef GDN2_RESIDENT
+    const unsigned blocks = unsigned(even_blocks(a.rows, rows_at_once(a.D), 256 * 4 * waves / workgroup_waves(a.D)));
     if (blocks == 0) return hipSuccess;
 #define GDN2_FWD(LPR, WPR, NI, MODE)                                                          \
     hipLaunchKernelGGL((block_norm_fwd_kernel<T, R, LPR, WPR, NI, MODE>), dim3(blocks),       \
@@ -186,7 +209,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutCall a, int64_t gro
         T* y = static_cast<T*>(a.y) + e;
         Eight<T> r;
         if (MODE == kWhole) {
-            r.load(x, true);
+            r.load(x);
         } else if (MODE == kRagged) {
             r.load_any(x - (whole ? 0 : 8 - rest));
             if (!whole) r.shift(8 - rest);

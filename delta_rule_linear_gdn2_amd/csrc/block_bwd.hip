@@ -55,25 +55,33 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
     Eight<T> u[NI], g[NI], dh[NI];
     Eight<R> x[NI], dx[NI];
     float tok = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        u[i].clear();
+        g[i].clear();
+        dh[i].clear();
+        x[i].clear();
+        dx[i].clear();
+    }
     auto load_stream = [&](int64_t row) {
-        const bool live = row < a.rows;
-        const int64_t at = (MODE != kRagged || live ? row : a.rows - 1) * a.D;
+        const bool live = row < a.rows, last = row >= a.rows - 1;
+        const int64_t at = row * a.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if (pre) {
-                grp[i].load(x[i], static_cast<const R*>(a.x) + at, a.D, live);
-                grp[i].load(dh[i], static_cast<const T*>(a.d_h) + at, a.D, live);
+                grp[i].load(x[i], static_cast<const R*>(a.x) + at, a.D, live, last);
+                grp[i].load(dh[i], static_cast<const T*>(a.d_h) + at, a.D, live, last);
             }
-            if (has_dx) grp[i].load(dx[i], static_cast<const R*>(a.d_x_out) + at, a.D, live);
+            if (has_dx) grp[i].load(dx[i], static_cast<const R*>(a.d_x_out) + at, a.D, live, last);
         }
     };
     auto load_block = [&](int64_t row) {
-        const bool live = row < a.rows;
-        const int64_t at = (MODE != kRagged || live ? row : a.rows - 1) * a.D;
+        const bool live = row < a.rows, last = row >= a.rows - 1;
+        const int64_t at = row * a.D;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            if (reads_u) grp[i].load(u[i], static_cast<const T*>(a.u) + at, a.D, live);
-            if (full_gate) grp[i].load(g[i], static_cast<const T*>(a.gate) + at, a.D, live);
+            if (reads_u) grp[i].load(u[i], static_cast<const T*>(a.u) + at, a.D, live, last);
+            if (full_gate) grp[i].load(g[i], static_cast<const T*>(a.gate) + at, a.D, live, last);
         }
         if (token_gate) tok = live ? load_as_f32(static_cast<const T*>(a.gate), row) : 0.f;
     };
@@ -83,7 +91,7 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
     load_block(base + slot);
     for (; base < a.rows; base += step) {
         const int64_t row = base + slot;
-        const bool live = row < a.rows;
+        const bool live = row < a.rows, last = row >= a.rows - 1;
 
         // t, the gradient of x'
         float t[NI][8];
@@ -92,8 +100,8 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
         for (int i = 0; i < NI; ++i) {
             if (pre) {
                 float xv[8], hv[8];
-                grp[i].settle(x[i], a.D, live);
-                grp[i].settle(dh[i], a.D, live);
+                grp[i].settle(x[i], a.D, last);
+                grp[i].settle(dh[i], a.D, last);
                 x[i].get(xv);
                 dh[i].get(hv);
 #pragma unroll
@@ -102,9 +110,9 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
                     s[1] = fmaf(wr[i][j] * hv[j], xv[j], s[1]);
                 }
             }
-            if (has_dx) grp[i].settle(dx[i], a.D, live);
-            if (reads_u) grp[i].settle(u[i], a.D, live);
-            if (full_gate) grp[i].settle(g[i], a.D, live);
+            if (has_dx) grp[i].settle(dx[i], a.D, last);
+            if (reads_u) grp[i].settle(u[i], a.D, last);
+            if (full_gate) grp[i].settle(g[i], a.D, last);
             if (post) {
                 float v[8];
                 u[i].get(v);
@@ -162,8 +170,8 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
 #pragma unroll
                 for (int j = 0; j < 8; ++j) t[i][j] = philox_keep(bits, j, a.drop.threshold) ? t[i][j] : 0.f;
             }
-            float uv[8] = {}, hat[8];
-            if (reads_u) u[i].get(uv);
+            float uv[8], hat[8];
+            u[i].get(uv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) hat[j] = uv[j] * ru;
             if (full_gate) {

@@ -94,7 +94,8 @@ __device__ __forceinline__ void load_weight(const float* w, const Group<MODE>& g
         return;
     }
     Eight<float> e;
-    group.load(e, w, D, true);
+    e.clear();
+    group.load(e, w, D, true, true);
     group.settle(e, D, true);
     e.get(v);
 }

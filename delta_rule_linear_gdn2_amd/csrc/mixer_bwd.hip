@@ -54,9 +54,12 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
         const bool on = r < a.rows;
         const int64_t e = r * DV + c0;
         Eight<T> ro, rg, ry;
-        ro.load(static_cast<const T*>(a.o) + e, on);
-        rg.load(static_cast<const T*>(a.gate) + e, on);
-        ry.load(static_cast<const T*>(a.d_y) + e, on);
+        if (on) ro.load(static_cast<const T*>(a.o) + e);
+        else ro.clear();
+        if (on) rg.load(static_cast<const T*>(a.gate) + e);
+        else rg.clear();
+        if (on) ry.load(static_cast<const T*>(a.d_y) + e);
+        else ry.clear();
         float o[8], g[8], y[8], dn[8], dg[8];
         ro.get(o);
         rg.get(g);
@@ -469,8 +472,8 @@ __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t 
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const int64_t at = (t + i < t1 ? t + i : t1 - 1) * stride;
-            rl[i].load(logit + at + chan, true);
-            rd[i].load(dg + at + chan, true);
+            rl[i].load(logit + at + chan);
+            rd[i].load(dg + at + chan);
         }
 #pragma unroll
         for (int i = 0; i < M; ++i) {

@@ -45,11 +45,12 @@ __device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn
 // Where the row length is a multiple of eight, each group is whole and at a
 // 16-byte boundary and loaded as it is.  In ragged rows a
 // group sits at any element boundary, which gfx950 takes for 16-byte accesses,
-// and the last one is short.  That one is loaded whole all the same, from the
-// row's last eight elements, and shifted into place when it is used: taken in
-// pieces, it would be waited for where it is loaded, and with it everything
-// loaded before.  It is stored in pieces of four, two and one.  Rows of under
-// eight elements are loaded in such pieces too.
+// and the last one is short.  That one is loaded whole all the same, with what
+// follows it, which is cleared when it is used (in the last row, from the row's
+// last eight elements, and shifted into place): taken in pieces, it would be
+// waited for where it is loaded, and with it everything loaded before.  It is
+// stored in pieces of four, two and one.  Rows of under eight elements are
+// loaded in such pieces too.
 //
 // STREAM in a store: past the caches, for outputs that no cache will hold until
 // they are read.
@@ -76,12 +77,8 @@ struct Eight;
 template <>
 struct Eight<bf16raw> {
     u32x4_t u;
-    // A whole group at a 16-byte boundary, or zeros.
-    __device__ __forceinline__ void load(const bf16raw* p, bool on)
-    {
-        if (on) u = *reinterpret_cast<const u32x4_t*>(p);
-        else u = u32x4_t{0, 0, 0, 0};
-    }
+    // A whole group at a 16-byte boundary.
+    __device__ __forceinline__ void load(const bf16raw* p) { u = *reinterpret_cast<const u32x4_t*>(p); }
     // A whole group at any boundary.
     __device__ __forceinline__ void load_any(const bf16raw* p) { u = *reinterpret_cast<const u32x4_any*>(p); }
     // The first n < 8 elements, zeros behind them.
@@ -104,6 +101,12 @@ struct Eight<bf16raw> {
 #pragma unroll
             for (int j = 0; j < 4; ++j) u[j] = (n & 6) == 2 * j ? v : u[j];
         }
+    }
+    // Keeps the first n elements.
+    __device__ __forceinline__ void first(int n)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] &= n > 2 * j + 1 ? 0xffffffffu : n > 2 * j ? 0xffffu : 0u;
     }
     __device__ __forceinline__ void clear() { u = u32x4_t{0, 0, 0, 0}; }
     // by < 8 elements down, zeros behind them.
@@ -145,14 +148,10 @@ struct Eight<bf16raw> {
 template <>
 struct Eight<float> {
     f32x4_t a, b;
-    __device__ __forceinline__ void load(const float* p, bool on)
+    __device__ __forceinline__ void load(const float* p)
     {
-        if (on) {
-            a = *reinterpret_cast<const f32x4_t*>(p);
-            b = *reinterpret_cast<const f32x4_t*>(p + 4);
-        } else {
-            a = b = f32x4_t{0, 0, 0, 0};
-        }
+        a = *reinterpret_cast<const f32x4_t*>(p);
+        b = *reinterpret_cast<const f32x4_t*>(p + 4);
     }
     __device__ __forceinline__ void load_any(const float* p)
     {
@@ -180,6 +179,14 @@ struct Eight<float> {
             a[2] = (n & 6) == 2 ? v : a[2];
             b[0] = (n & 6) == 4 ? v : b[0];
             b[2] = (n & 6) == 6 ? v : b[2];
+        }
+    }
+    __device__ __forceinline__ void first(int n)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j >= n) a[j] = 0.f;
+            if (j + 4 >= n) b[j] = 0.f;
         }
     }
     __device__ __forceinline__ void clear() { a = b = f32x4_t{0, 0, 0, 0}; }
@@ -241,12 +248,12 @@ constexpr int kWhole = 0, kRagged = 1, kTiny = 2;
 inline int row_mode(int64_t D) { return D % 8 == 0 ? kWhole : D > 8 ? kRagged : kTiny; }
 
 // A lane's group of eight of a row of D elements.  In a ragged row it is whole,
-// short (the row's last D % 8 elements) or behind the row.  How short, and so how
-// far its load is shifted and which pieces are stored, is the same for every
-// row and lane, which makes those branches scalar.
+// short (the row's last D % 8 elements) or behind the row.  How short, and so
+// what is cleared and which pieces are stored, is the same for every row and
+// lane, which makes those branches scalar.
 template <int MODE>
 struct Group {
-    uint32_t col, from;  // its first column, and where it is loaded
+    uint32_t col, from;  // its first column, and where it is loaded in the last row
     int kind;            // 0 whole, 1 short, 2 behind the row
     __device__ __forceinline__ void init(uint32_t first, uint32_t D)
     {
@@ -254,21 +261,27 @@ struct Group {
         kind = first >= D ? 2 : MODE == kWhole || first + 8 <= D ? 0 : 1;
         if (MODE == kRagged && kind != 0) from = D - 8;
     }
-    // The elements from row[0 .. D).  `on`: the row exists; a ragged row that does
-    // not is loaded nevertheless, from one that does, and settle() clears it.
+    // The elements from row[0 .. D) into e, which was cleared once before its first
+    // load: groups behind the row are never loaded and stay zero.  `on`: the row
+    // exists.  `last`: nothing may be read behind it.  A ragged row's short group
+    // is in place after settle().
     template <typename T>
-    __device__ __forceinline__ void load(Eight<T>& e, const T* row, uint32_t D, bool on) const
+    __device__ __forceinline__ void load(Eight<T>& e, const T* row, uint32_t D, bool on, bool last) const
     {
-        if (MODE == kWhole) e.load(row + col, on && kind == 0);
-        else if (MODE == kRagged) e.load_any(row + from);
-        else e.load_pieces(row + col, on ? int(D) - int(col) : 0);
+        if (!on) {
+            e.clear();
+        } else if (kind != 2) {
+            if (MODE == kWhole) e.load(row + col);
+            else if (MODE == kRagged) e.load_any(row + (last ? from : col));
+            else e.load_pieces(row + col, int(D) - int(col));
+        }
     }
     template <typename T>
-    __device__ __forceinline__ void settle(Eight<T>& e, uint32_t D, bool on) const
+    __device__ __forceinline__ void settle(Eight<T>& e, uint32_t D, bool last) const
     {
-        if (MODE != kRagged) return;
-        if (kind == 1) e.shift(8 - int(D % 8));
-        if (kind == 2 || !on) e.clear();
+        if (MODE != kRagged || kind != 1) return;
+        if (last) e.shift(8 - int(D % 8));
+        else e.first(int(D % 8));
     }
     template <typename T>
     __device__ __forceinline__ void store(const Eight<T>& e, T* row, uint32_t D, bool on) const
@@ -297,14 +310,17 @@ __device__ __forceinline__ u32x4_t philox4x32(uint64_t block, uint64_t offset, u
 {
     uint32_t a = uint32_t(block), b = uint32_t(block >> 32), c = uint32_t(offset), d = uint32_t(offset >> 32);
     uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+    // The round keys are two scalar additions a round.  Without this the compiler
+    // computes all twenty before a kernel's row loop, and has to park them in
+    // vector lanes.
+    asm volatile("" : "+s"(k0), "+s"(k1));
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
         const uint64_t p = uint64_t(a) * 0xD2511F53u, q = uint64_t(c) * 0xCD9E8D57u;
-        const uint32_t na = uint32_t(q >> 32) ^ b ^ k0, nc = uint32_t(p >> 32) ^ d ^ k1;
+        a = __builtin_amdgcn_bitop3_b32(uint32_t(q >> 32), b, k0, 0x96);  // exclusive or of the three
+        c = __builtin_amdgcn_bitop3_b32(uint32_t(p >> 32), d, k1, 0x96);
         b = uint32_t(q);
         d = uint32_t(p);
-        a = na;
-        c = nc;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
