@@ -518,8 +518,8 @@ def gdn2_mixer_epilogue(o, gate, weight, *, eps=1e-5, act="sigmoid", out=None, s
 def _on_stream(f):
     """Runs a call on ``stream`` (default: the current stream of its tensors'
     device), with that device current.  What the call allocates (outputs,
-    workspace) belongs to that stream, so memory another stream is still
-    using is never handed to it, nor its own to another stream too early."""
+    workspace) belongs to that stream, and the caller's tensors are recorded on
+    it: memory that one stream still uses is never handed to another."""
 
     @functools.wraps(f)
     def call(first, *args, stream=None, **kw):
@@ -528,6 +528,9 @@ def _on_stream(f):
         if stream is not None:
             if stream.device != first.device:
                 raise ValueError(f"stream: on {stream.device}, the tensors are on {first.device}")
+            for t in (first, *args, *kw.values()):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
             with torch.cuda.stream(stream):
                 return f(first, *args, **kw)
         index = first.get_device()
@@ -600,6 +603,7 @@ def _rows(name, t, shape):
 def _random(seed, offset, offset_device, index):
     if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
         raise ValueError(f"seed and offset must be in [0, 2^64) (got {seed}, {offset})")
+    seed, offset = int(seed), int(offset)
     if offset_device is None:
         return seed, offset, None
     import torch
@@ -667,6 +671,8 @@ def gdn2_block_norm_fwd(x, u=None, *, gate=None, gate_layout="none", gate_act="s
     rdt = x.dtype
     dt = u.dtype if u is not None else dtype or rdt
     if u is not None:
+        if dtype is not None and dtype != dt:
+            raise TypeError(f"dtype: h has u's type, {dt} (got {dtype})")
         x_out = _buffer("x_out", x_out, x, shape, rdt, index)
     elif x_out is not None:
         raise ValueError("x_out: there is none without u")

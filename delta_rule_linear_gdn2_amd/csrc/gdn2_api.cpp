@@ -530,6 +530,8 @@ size_t prologue_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t dk, int32
     return align256(size_t(B) * size_t(runs) * size_t(H) * size_t(2 * dk + dv) * size_t(K) * 4);
 }
 
+constexpr int32_t kMaxHeads = 1 << 20;  // a token's channels and filter taps stay far inside 32 bits
+
 gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&conv)[3], const void* const (&logit)[2],
                                const float* conv_state_in, const void* const (&d_out)[3],
                                const void* const (&d_gate)[2], const float* d_state_out, void* const (&d_x)[3],
@@ -543,6 +545,7 @@ gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&c
     if (cu_seqlens && (B != 1 || num_seqs <= 0)) return GDN2_ERR_BAD_SHAPE;
     if (!(eps_l2 >= 0.f)) return GDN2_ERR_BAD_SHAPE;
     if (!supported_head(dk) || !supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
+    if (H > kMaxHeads) return GDN2_ERR_BAD_SHAPE;
     const int32_t N = cu_seqlens ? num_seqs : B;
     if (T > 0)
         for (const void* p : {x[0], x[1], x[2], static_cast<const void*>(conv[0]), static_cast<const void*>(conv[1]),

@@ -361,7 +361,7 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
             }
     };
 
-    const int last = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;  // tokens past t1 complete this run's gradients
+    const int64_t last = int64_t(t1) + K - 1 < a.T ? t1 + K - 1 : a.T;  // tokens past t1 complete this run's gradients
     // a whole step inside one sequence, neither its first K - 1 tokens nor its last one
     auto whole = [&](int64_t t) { return t + kStep <= last && t + kStep < eos && t - (K - 1) >= bos; };
     Ch rx[kStep], rg[kStep];

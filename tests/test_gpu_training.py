@@ -332,6 +332,56 @@ def test_block_step_in_a_replayed_graph():
     assert not torch.equal(masks[0], masks[1])
 
 
+def test_calls_without_rows():
+    """Nothing to read, and the gradients of shared inputs are zero."""
+    import torch
+
+    for D in (64, 75):
+        e = torch.empty((0, D), dtype=torch.bfloat16, device="cuda")
+        w, g = torch.ones(D, device="cuda"), torch.ones(D, device="cuda")
+        how = dict(gate=g, gate_layout="channel", weight_post=w, weight_pre=w, dropout_p=0.1, seed=1)
+        x_out, h = binding.gdn2_block_norm_fwd(e, e.clone(), **how)
+        assert x_out.shape == h.shape == (0, D)
+        got = binding.gdn2_block_norm_bwd(e, e.clone(), e.clone(), e.clone(), **how)
+        for n in ("d_gate", "d_weight_post", "d_weight_pre"):
+            assert got[n].shape == (D,) and not got[n].any()
+        assert binding.gdn2_dropout(e, 0.1, 1).shape == (0, D)
+    e = torch.empty((0, 64), device="cuda")
+    assert not binding.gdn2_mixer_epilogue_bwd(e, e.clone(), torch.ones(64, device="cuda"), e.clone())["d_weight"].any()
+
+
+def test_calls_at_once_on_two_streams():
+    """Two streams run the same backward calls side by side, many times over: each result is that of the call alone."""
+    import torch
+
+    blocks = [Block(548 + k, 2000, 264, "bf16", "f32", "channel", "silu", p=0.3) for k in range(2)]
+    outs = [b.fwd()[0] for b in blocks]
+    refs = [b.bwd(x) for b, x in zip(blocks, outs)]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [binding.gdn2_block_norm_bwd(x, b.t["u"], b.t["d_x_out"], b.t["d_h"], stream=s, **b.how)
+               for b, x, s in zip(blocks, outs, streams)]
+    torch.cuda.synchronize()
+    for g, ref in zip(got, refs):
+        for name, v in ref.items():
+            assert torch.equal(g[name], v), name
+
+
+def test_one_leading_axis_or_several():
+    """A call over [B, T, D] is the call over its rows."""
+    import torch
+
+    b = Block(546, 24, 96, "bf16", "f32", "token", "silu", p=0.2)
+    x_out, h = b.fwd()
+    cut = lambda t: t.view(4, 6, *t.shape[1:])  # noqa: E731
+    how = {**b.how, "gate": cut(b.t["gate"])}
+    y, h3 = binding.gdn2_block_norm_fwd(cut(b.t["x"]), cut(b.t["u"]), **how)
+    assert torch.equal(y, cut(x_out)) and torch.equal(h3, cut(h))
+    one = binding.gdn2_dropout(b.t["x"], 0.2, 3)
+    assert torch.equal(binding.gdn2_dropout(cut(b.t["x"]), 0.2, 3), cut(one))
+
+
 def test_calls_on_another_stream_and_repeated():
     """On a stream of its own, twice: bit for bit what the current stream gives."""
     import torch

@@ -154,6 +154,7 @@ PRO = dict({n: fake(i) for i, n in enumerate(PRO_NAMES)}, cu=None, B=2, T=64, H=
     (dict(T=-1), SHAPE),
     (dict(cu=fake(40), num_seqs=3), SHAPE),               # packed with B = 2
     (dict(cu=fake(40), B=1, num_seqs=0), SHAPE),
+    (dict(H=(1 << 20) + 1), SHAPE),
     (dict(dk=96), UNSUP),
     (dict(cq=None), NULLP),
     (dict(dw=None), NULLP),
@@ -222,6 +223,7 @@ def test_binding_refuses_cpu_tensors():
     (ValueError, dict(offset=1 << 64)),
     (TypeError, dict(offset_device=_x(1))),
     (TypeError, dict(u=_x(3, 16, dtype=torch.float16))),
+    (TypeError, dict(dtype=torch.bfloat16)),                                  # h has u's type
 ])
 def test_block_norm_fwd_binding_rejects(error, kw):
     with pytest.raises(error, match="^(?!.*must be on a GPU)"):
