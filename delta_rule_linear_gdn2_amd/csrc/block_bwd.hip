@@ -1,14 +1,16 @@
 // Gradients of the step from one block of a layer to the next (formulas:
 // block.hip), for gfx950.
 //
-// HBM-bound in its bytes (16 a bf16 element with a full gate), with about 65
-// vector instructions an element beside them, so what counts is wavefronts
-// enough to hide both.  A row is held in registers once: the stream's side (x',
-// dh, dx') is read first and makes t, and its registers take the next row's
-// loads while the block's side (u, gate) is worked on, and the other way round,
-// so the next row is always on its way without a second set of registers.  Two
-// sums over the row, one barrier each where it spans wavefronts.  The weights'
-// column sums stay in registers over all rows of a workgroup.
+// 16 bytes of HBM an element (bf16, full gate) and about 56 vector instructions
+// (13 of them the dropout's bits, 12 the gate): at 32768 x 2048 HBM bounds it (206 us
+// a call, 1.08 GB, the rate of a large copy), in rows that leave lanes idle the
+// instructions do (24424 rows of 1371: 131 us, 81% of that rate).  So a row is read
+// once and held in registers: the stream's side (x', dh, dx') makes t, and its
+// registers take the next row's loads while the block's side (u, gate) is worked
+// on, and the other way round, so the next row is always on its way without a
+// second set of registers.  Two sums over the row, one barrier each where it
+// spans wavefronts.  The weights' column sums stay in registers over all rows of
+// a workgroup.
 #include "block_device.hpp"
 
 namespace gdn2 {
@@ -18,6 +20,18 @@ namespace {
 // where a lane holds eight channels, two (256) at sixteen; sixteen wavefronts
 // are a workgroup of four a SIMD anyway.
 constexpr int bwd_waves_per_simd(int WPR, int NI) { return NI == 1 ? 3 : WPR == 16 ? 4 : 2; }
+
+// The backward pass's covers: three wavefronts for rows of 1025 to 1536 channels,
+// whose four would idle a third of their lanes and then bound it by its vector
+// instructions (24424 rows of 1371, bf16, gate and dropout: 150 us with four, 131
+// with three; 24385 of 1376: 138 and 116).  The forward pass, with fewer of them,
+// is faster with four.
+#define GDN2_BWD_COVER(D, F)                             \
+    do {                                                 \
+        if ((D) <= 1024 || (D) > 1536) GDN2_COVER(D, F); \
+        else if (row_mode(D) == kWhole) F(64, 3, 1, kWhole); \
+        else F(64, 3, 1, kRagged);                       \
+    } while (0)
 
 // CHANNEL: the gate is one value per channel, whose gradient is a third column
 // sum (without it those registers are free).  MODE: how rows lie.
@@ -291,7 +305,7 @@ hipError_t bwd_typed(const BlockNormBwdArgs& a, hipStream_t stream)
             hipLaunchKernelGGL((block_norm_bwd_kernel<T, R, LPR, WPR, NI, MODE, false>), dim3(blocks),    \
                                dim3(Cover<LPR, WPR, NI>::kThreads), 0, stream, a);                        \
     } while (0)
-        GDN2_COVER(a.D, GDN2_BWD);
+        GDN2_BWD_COVER(a.D, GDN2_BWD);
 #undef GDN2_BWD
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -314,12 +328,14 @@ hipError_t bwd_typed(const BlockNormBwdArgs& a, hipStream_t stream)
 
 int64_t block_bwd_partials(int64_t rows, int32_t D)
 {
-    // as many workgroups as are resident at once on 256 compute units of four SIMDs
-    int waves = 1;
-#define GDN2_RESIDENT(LPR, WPR, NI, MODE) waves = bwd_waves_per_simd(WPR, NI)
-    GDN2_COVER(D, GDN2_RESIDENT);
-#undef GDN2_RESIDENT
-    return even_blocks(rows, rows_at_once(D), 256 * 4 * waves / workgroup_waves(D));
+    // as many workgroups as are resident at once
+    int at_once = 1, resident = 1;
+#define GDN2_PLAN(LPR, WPR, NI, MODE)          \
+    at_once = Cover<LPR, WPR, NI>::kRows,      \
+    resident = kSimds * bwd_waves_per_simd(WPR, NI) / Cover<LPR, WPR, NI>::kWaves
+    GDN2_BWD_COVER(D, GDN2_PLAN);
+#undef GDN2_PLAN
+    return even_blocks(rows, at_once, resident);
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormBwdArgs& a, bool bf16, bool residual_bf16, hipStream_t stream)

@@ -42,7 +42,7 @@ __device__ __forceinline__ void act_values(int act, const float* g, float* f, fl
 // groups of eight channels a lane.
 template <int LPR, int WPR, int NI>
 struct Cover {
-    static constexpr int kThreads = WPR <= 4 ? 256 : WPR * 64;
+    static constexpr int kThreads = WPR == 1 || WPR == 2 ? 256 : WPR * 64;
     static constexpr int kWaves = kThreads / 64;
     static constexpr int kRowLanes = LPR * WPR;
     static constexpr int kRows = kThreads / kRowLanes;  // rows at a time per workgroup
@@ -129,23 +129,7 @@ __device__ __forceinline__ void load_weight(const float* w, const Group<MODE>& g
         else F(64, 16, 2, MODE);                   \
     } while (0)
 
-inline int rows_at_once(int32_t D)
-{
-    int n = 1;
-#define GDN2_ROWS(LPR, WPR, NI, MODE) n = Cover<LPR, WPR, NI>::kRows
-    GDN2_COVER(D, GDN2_ROWS);
-#undef GDN2_ROWS
-    return n;
-}
-
-inline int workgroup_waves(int32_t D)
-{
-    int n = 1;
-#define GDN2_WAVES(LPR, WPR, NI, MODE) n = Cover<LPR, WPR, NI>::kWaves
-    GDN2_COVER(D, GDN2_WAVES);
-#undef GDN2_WAVES
-    return n;
-}
+constexpr int kSimds = 256 * 4;  // compute units of an MI355X, four SIMDs each
 
 // Workgroups of a launch over `rows` rows that walk the same number of rounds of
 // `at_once` rows each, at most `most` of them.

@@ -102,8 +102,8 @@ TYPES = [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")]
 
 
 # every cover of a row (lane group, wavefront, several), whole groups of eight and ragged ones, a group more than a cover holds
-@pytest.mark.parametrize("D", [1, 7, 16, 64, 65, 200, 256, 333, 512, 1000, 1001, 1024, 1371, 2048, 2050, 4096, 4104, 5461,
-                               8192, 9001, 16384])
+@pytest.mark.parametrize("D", [1, 7, 8, 9, 16, 31, 32, 64, 65, 96, 200, 256, 333, 512, 1000, 1001, 1024, 1200, 1371, 1536, 2047,
+                               2048, 2050, 4096, 4104, 5461, 6000, 8192, 9001, 16384])
 @pytest.mark.parametrize("dtype,res", TYPES)
 def test_block_widths(D, dtype, res):
     rows = 37 if D <= 2048 else 5
