@@ -514,6 +514,25 @@ def gdn2_mixer_epilogue(o, gate, weight, *, eps=1e-5, act="sigmoid", out=None, s
 
 # --- training operators ------------------------------------------------------
 
+# A small call's time is this module's own: torch is imported once (at the first
+# call, not with the package), sizes are asked of the library once per shape, and
+# whatever can only raise comes after one comparison that says it need not.
+torch = None
+_CODES = {}
+
+
+def _import_torch():
+    global torch
+    import torch as module
+
+    torch = module
+    _CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
+    load()
+
+
+def _code(dt):
+    return _CODES[dt] if dt in _CODES else _dtype_code(dt)  # the latter raises
+
 
 def _on_stream(f):
     """Runs a call on ``stream`` (default: the current stream of its tensors'
@@ -523,8 +542,8 @@ def _on_stream(f):
 
     @functools.wraps(f)
     def call(first, *args, stream=None, **kw):
-        import torch
-
+        if torch is None:
+            _import_torch()
         if stream is not None:
             if stream.device != first.device:
                 raise ValueError(f"stream: on {stream.device}, the tensors are on {first.device}")
@@ -546,11 +565,9 @@ def _run(name, index, *args):
     """Calls the C function on device ``index``'s current stream (its handle
     alone: building the stream object takes longer than all checks); raises
     what it refuses."""
-    import torch
-
     if index < 0:
         raise ValueError(f"{name}: tensors must be on a GPU")
-    rc = getattr(_LIB or load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    rc = getattr(_LIB, name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != GDN2_OK:
         raise Gdn2Error(rc, name)
 
@@ -558,8 +575,6 @@ def _run(name, index, *args):
 def _expect(name, t, shape, dtype, index):
     """_check at a fifth of its time where nothing is wrong."""
     if not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
-        import torch
-
         _check(name, t, tuple(shape), dtype, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
 
 
@@ -571,23 +586,21 @@ def _buffer(name, t, like, shape, dtype, index):
     """The caller's output tensor, checked, or a new one like ``like`` (of that
     shape, type and device)."""
     if t is None:
-        import torch
-
         return torch.empty_like(like)
     _expect(name, t, shape, dtype, index)
     return t
 
 
-def _workspace(t, nbytes, dev):
-    import torch
-
+def _workspace(t, nbytes, like):
+    """The caller's workspace, checked, or a new one on ``like``'s device."""
     if not nbytes:
         return None, 0
     if t is None:
-        t = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    elif t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+        return like.new_empty(nbytes, dtype=torch.uint8), nbytes
+    dev = like.device
+    if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
         raise ValueError(f"workspace: must be contiguous uint8 on {dev}")
-    elif t.numel() < nbytes:
+    if t.numel() < nbytes:
         raise ValueError(f"workspace of {t.numel()} bytes < {nbytes}")
     return t, t.numel()
 
@@ -606,8 +619,6 @@ def _random(seed, offset, offset_device, index):
     seed, offset = int(seed), int(offset)
     if offset_device is None:
         return seed, offset, None
-    import torch
-
     _expect("offset_device", offset_device, (1,), torch.int64, index)
     return seed, offset, offset_device.data_ptr()
 
@@ -619,8 +630,6 @@ BLOCK_GATE_ACTS = {"sigmoid": 0, "silu": 1, "identity": 2}
 def _block_inputs(x, u, gate, gate_layout, gate_act, weight_post, weight_pre):
     """Checks the inputs that the block norm's two directions share; returns
     their rows, shape and device index, and the codes of gate and activation."""
-    import torch
-
     shape, index = x.shape, x.get_device()
     rows = _rows("x", x, shape)
     if u is not None:
@@ -687,12 +696,13 @@ def gdn2_block_norm_fwd(x, u=None, *, gate=None, gate_layout="none", gate_act="s
         _expect("h", h, shape, dt, index)
     _run("gdn2_block_norm_fwd", index, x.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
          _addr(x_out), _addr(h), rows, shape[-1], eps, residual_scale, layout, act, dropout_p,
-         *_random(seed, offset, offset_device, index), _dtype_code(dt), _dtype_code(rdt))
+         *_random(seed, offset, offset_device, index), _code(dt), _code(rdt))
     return (x if u is None else x_out), h
 
 
+@functools.lru_cache(maxsize=256)
 def gdn2_block_norm_bwd_workspace_bytes(rows, D) -> int:
-    return int((_LIB or load()).gdn2_block_norm_bwd_workspace_bytes(rows, D))
+    return int(load().gdn2_block_norm_bwd_workspace_bytes(rows, D))
 
 
 @_on_stream
@@ -708,12 +718,10 @@ def gdn2_block_norm_bwd(x_out, u, d_x_out, d_h, *, gate=None, gate_layout="none"
     d_weight_pre), None in the place of what has no input or is not wanted.  d_x
     may be d_x_out (in place).  ``workspace`` (uint8) is allocated when not given.
     """
-    import torch
-
     rows, shape, index, layout, act = _block_inputs(x_out, u, gate, gate_layout, gate_act, weight_post, weight_pre)
     D, rdt = shape[-1], x_out.dtype
     dt = u.dtype if u is not None else d_h.dtype if d_h is not None else rdt
-    code = _dtype_code(dt)
+    code = _code(dt)
     if d_x_out is not None:
         _expect("d_x_out", d_x_out, shape, rdt, index)
     if (d_h is None) != (weight_pre is None):
@@ -732,11 +740,11 @@ def gdn2_block_norm_bwd(x_out, u, d_x_out, d_h, *, gate=None, gate_layout="none"
     d_post = torch.empty_like(weight_post) if want_d_weights and weight_post is not None else None
     d_pre = torch.empty_like(weight_pre) if want_d_weights and weight_pre is not None else None
     sums = d_post is not None or d_pre is not None or (d_gate is not None and layout == 1)
-    workspace, ws_bytes = _workspace(workspace, gdn2_block_norm_bwd_workspace_bytes(rows, D) if sums else 0, x_out.device)
+    workspace, ws_bytes = _workspace(workspace, gdn2_block_norm_bwd_workspace_bytes(rows, D) if sums else 0, x_out)
     _run("gdn2_block_norm_bwd", index, x_out.data_ptr(), _addr(u), _addr(gate), _addr(weight_post), _addr(weight_pre),
          _addr(d_x_out), _addr(d_h), d_x.data_ptr(), _addr(d_u), _addr(d_gate), _addr(d_post), _addr(d_pre), rows, D,
          eps, residual_scale, layout, act, dropout_p, *_random(seed, offset, offset_device, index), code,
-         _dtype_code(rdt), _addr(workspace), ws_bytes)
+         _code(rdt), _addr(workspace), ws_bytes)
     return {"d_x": d_x, "d_u": d_u, "d_gate": d_gate, "d_weight_post": d_post, "d_weight_pre": d_pre}
 
 
@@ -752,10 +760,11 @@ def gdn2_dropout(x, p, seed, offset=0, *, offset_device=None, out=None):
     rows = _rows("x", x, shape)
     out = _buffer("out", out, x, shape, dt, index)
     _run("gdn2_dropout", index, x.data_ptr(), out.data_ptr(), rows, shape[-1], p,
-         *_random(seed, offset, offset_device, index), _dtype_code(dt))
+         *_random(seed, offset, offset_device, index), _code(dt))
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv) -> int:
     return int(load().gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv))
 
@@ -765,11 +774,9 @@ def gdn2_mixer_epilogue_bwd(o, gate, weight, d_y, *, eps=1e-5, act="sigmoid", wa
     """Gradients of gdn2_mixer_epilogue for the loss <d_y, y>: dict(d_o, d_gate,
     d_weight), d_weight None when not wanted.  ``workspace`` (uint8) is
     allocated when not given."""
-    import torch
-
     shape, index, dt = o.shape, o.get_device(), o.dtype
     rows = _rows("o", o, shape)
-    dv, code = shape[-1], _dtype_code(dt)
+    dv, code = shape[-1], _code(dt)
     _expect("gate", gate, shape, dt, index)
     _expect("weight", weight, shape[-1:], torch.float32, index)
     _expect("d_y", d_y, shape, dt, index)
@@ -778,13 +785,14 @@ def gdn2_mixer_epilogue_bwd(o, gate, weight, d_y, *, eps=1e-5, act="sigmoid", wa
     d_o, d_gate = torch.empty_like(o), torch.empty_like(o)
     d_weight = torch.empty_like(weight) if want_d_weight else None
     workspace, ws_bytes = _workspace(workspace, gdn2_mixer_epilogue_bwd_workspace_bytes(rows, dv) if want_d_weight else 0,
-                                     o.device)
+                                     o)
     _run("gdn2_mixer_epilogue_bwd", index, o.data_ptr(), gate.data_ptr(), weight.data_ptr(), d_y.data_ptr(),
          d_o.data_ptr(), d_gate.data_ptr(), _addr(d_weight), rows, dv, eps, GATE_ACTS[act], code, _addr(workspace),
          ws_bytes)
     return {"d_o": d_o, "d_gate": d_gate, "d_weight": d_weight}
 
 
+@functools.lru_cache(maxsize=256)
 def gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, kernel_size) -> int:
     return int(load().gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, kernel_size))
 
@@ -803,13 +811,11 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
     d_conv_state), None in the place of what is not wanted.  ``workspace``
     (uint8) is allocated when not given.
     """
-    import torch
-
     key, value, index, dt = xq.shape, xv.shape, xq.get_device(), xq.dtype
     if len(key) != 4 or len(value) != 4:
         raise ValueError(f"xq, xk, xv: [B, T, H, d] (got {tuple(key)}, {tuple(value)})")
     B, T, H, dk = key
-    dv, K, code = value[3], conv_q.shape[-1], _dtype_code(dt)
+    dv, K, code = value[3], conv_q.shape[-1], _code(dt)
     N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
     for name, t in (("xq", xq), ("xk", xk), ("b_logit", b_logit), ("d_q", d_q), ("d_k", d_k), ("d_b", d_b)):
         _expect(name, t, key, dt, index)
@@ -829,7 +835,7 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
     out["d_b_logit"], out["d_w_logit"] = torch.empty_like(b_logit), torch.empty_like(w_logit)
     out["d_conv_state"] = conv_q.new_empty(st_shape) if output_d_conv_state else None
     need = gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, K) if want_d_conv else 0
-    workspace, ws_bytes = _workspace(workspace, need, xq.device)
+    workspace, ws_bytes = _workspace(workspace, need, xq)
     _run("gdn2_mixer_prologue_bwd", index, xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), conv_q.data_ptr(),
          conv_k.data_ptr(), conv_v.data_ptr(), b_logit.data_ptr(), w_logit.data_ptr(), _addr(conv_state),
          d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), d_b.data_ptr(), d_w.data_ptr(), _addr(d_conv_state_out),
