@@ -817,10 +817,12 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
     B, T, H, dk = key
     dv, K, code = value[3], conv_q.shape[-1], _code(dt)
     N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    for name, t in (("xq", xq), ("xk", xk), ("b_logit", b_logit), ("d_q", d_q), ("d_k", d_k), ("d_b", d_b)):
-        _expect(name, t, key, dt, index)
-    for name, t in (("xv", xv), ("w_logit", w_logit), ("d_v", d_v), ("d_w", d_w)):
-        _expect(name, t, (B, T, H, dv), dt, index)
+    for want, tensors in ((key, (xq, xk, b_logit, d_q, d_k, d_b)), ((B, T, H, dv), (xv, w_logit, d_v, d_w))):
+        for t in tensors:
+            if not (t.shape == want and t.dtype is dt and t.get_device() == index and t.is_contiguous()):
+                name = next(n for n, v in dict(xq=xq, xk=xk, b_logit=b_logit, d_q=d_q, d_k=d_k, d_b=d_b, xv=xv,
+                                               w_logit=w_logit, d_v=d_v, d_w=d_w).items() if v is t)
+                _expect(name, t, want, dt, index)
     for name, t, width in (("conv_q", conv_q, dk), ("conv_k", conv_k, dk), ("conv_v", conv_v, dv)):
         _expect(name, t, (H * width, K), torch.float32, index)
     st_shape = (N, H * (2 * dk + dv), K - 1)
@@ -829,10 +831,10 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
             _expect(name, t, st_shape, torch.float32, index)
     if cu_seqlens is not None:
         _expect("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index)
-    out = {"d_xq": torch.empty_like(xq), "d_xk": torch.empty_like(xk), "d_xv": torch.empty_like(xv)}
-    for name, w in (("d_conv_q", conv_q), ("d_conv_k", conv_k), ("d_conv_v", conv_v)):
-        out[name] = torch.empty_like(w) if want_d_conv else None
-    out["d_b_logit"], out["d_w_logit"] = torch.empty_like(b_logit), torch.empty_like(w_logit)
+    new = torch.empty_like
+    out = {"d_xq": new(xq), "d_xk": new(xk), "d_xv": new(xv),
+           "d_conv_q": new(conv_q) if want_d_conv else None, "d_conv_k": new(conv_k) if want_d_conv else None,
+           "d_conv_v": new(conv_v) if want_d_conv else None, "d_b_logit": new(b_logit), "d_w_logit": new(w_logit)}
     out["d_conv_state"] = conv_q.new_empty(st_shape) if output_d_conv_state else None
     need = gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, K) if want_d_conv else 0
     workspace, ws_bytes = _workspace(workspace, need, xq)

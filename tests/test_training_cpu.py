@@ -256,3 +256,29 @@ def test_public_names():
                  "gdn2_mixer_prologue_bwd"):
         assert name in pkg.__all__ and getattr(pkg, name) is getattr(binding, name)
         assert isinstance(getattr(binding.load(), name), ctypes._CFuncPtr)
+
+
+def _prologue(**kw):
+    B, T, H, dk, dv, K = 2, 3, 2, 32, 64, 4
+    z = dict(xq=_x(B, T, H, dk), xk=_x(B, T, H, dk), xv=_x(B, T, H, dv), conv_q=_x(H * dk, K), conv_k=_x(H * dk, K),
+             conv_v=_x(H * dv, K), b_logit=_x(B, T, H, dk), w_logit=_x(B, T, H, dv), d_q=_x(B, T, H, dk),
+             d_k=_x(B, T, H, dk), d_v=_x(B, T, H, dv), d_b=_x(B, T, H, dk), d_w=_x(B, T, H, dv))
+    named = {n: kw.pop(n) for n in list(kw) if n not in z}
+    return binding.gdn2_mixer_prologue_bwd(*{**z, **kw}.values(), **named)
+
+
+@pytest.mark.parametrize("error,match,kw", [
+    (ValueError, "d_k: shape", dict(d_k=_x(2, 3, 2, 31))),
+    (ValueError, "w_logit: shape", dict(w_logit=_x(2, 3, 2, 32))),
+    (TypeError, "xv: dtype", dict(xv=_x(2, 3, 2, 64, dtype=torch.bfloat16))),
+    (ValueError, "d_b: must be contiguous", dict(d_b=_x(2, 3, 32, 2).transpose(2, 3))),
+    (ValueError, "conv_v: shape", dict(conv_v=_x(64, 4))),
+    (TypeError, "conv_q: dtype", dict(conv_q=_x(64, 4, dtype=torch.bfloat16))),
+    (ValueError, "conv_state: shape", dict(conv_state=_x(2, 256, 4))),
+    (TypeError, "cu_seqlens: dtype", dict(cu_seqlens=torch.zeros(3, dtype=torch.int64))),
+    (ValueError, r"\[B, T, H, d\]", dict(xv=_x(2, 3, 128))),
+    (ValueError, "must be on a GPU", dict()),
+])
+def test_mixer_prologue_bwd_binding_rejects(error, match, kw):
+    with pytest.raises(error, match=match):
+        _prologue(**kw)
