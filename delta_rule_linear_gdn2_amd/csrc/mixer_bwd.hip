@@ -113,7 +113,6 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
 }
 
 constexpr int64_t kEpiBlocks = 1024;
-constexpr int64_t kWantWaves = 1024;
 
 template <typename T>
 hipError_t epilogue_typed(const EpilogueBwdArgs& a, hipStream_t stream)
@@ -148,6 +147,18 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int32_t T, 
         if (c <= t) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Tokens [t0, t1) of run `run` that some sequence owns (packed input may end in
+// padding, which is neither read nor written); t1 <= t0: none.
+__device__ __forceinline__ void owned_tokens(const PrologueBwdArgs& a, int64_t run, int& t0, int& t1)
+{
+    t0 = int(run * a.run);
+    t1 = a.T - t0 > a.run ? t0 + a.run : a.T;
+    if (!a.cu_seqlens) return;
+    const int first = a.cu_seqlens[0], end = a.cu_seqlens[a.N];
+    t0 = first > t0 ? first : t0;
+    t1 = end < t1 ? end : t1;
 }
 
 // CPL consecutive channels of a row, as loaded: eight, four or two (bf16 stays
@@ -246,7 +257,8 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
     const int h = int(wid % ng) * HPW + lane / LPH;
     if (h >= a.H) return;  // lanes past the last head share no sum with live ones
     const int64_t run = (wid / ng) % nruns, brow = wid / ng / nruns;
-    const int t0 = int(run * a.run), t1 = a.T - t0 > a.run ? t0 + a.run : a.T;
+    int t0, t1;
+    owned_tokens(a, run, t0, t1);
     const int K = KM <= 4 ? KM : a.K, low = KM - K;
     const int chan = h * D + (lane % LPH) * CPL;  // first channel within the path
     const int64_t stride = int64_t(a.H) * D, row0 = brow * a.T * stride;
@@ -367,7 +379,8 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
             }
     };
 
-    const int64_t last = int64_t(t1) + K - 1 < a.T ? t1 + K - 1 : a.T;  // tokens past t1 complete this run's gradients
+    // tokens past t1 complete this run's gradients
+    const int64_t last = t0 >= t1 ? t0 : int64_t(t1) + K - 1 < a.T ? t1 + K - 1 : a.T;
     // a whole step inside one sequence, neither its first K - 1 tokens nor its last one
     auto whole = [&](int64_t t) { return t + kStep <= last && t + kStep < eos && t - (K - 1) >= bos; };
     Ch rx[kStep], rg[kStep];
@@ -378,7 +391,7 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
             rg[i].load(dout + (t + i) * stride + chan);
         }
     };
-    restart(t0);
+    if (t0 < t1) restart(t0);
     int64_t ahead = -1;  // the step whose loads are in flight
     for (int64_t t = t0; t < last;) {
         if (whole(t)) {
@@ -467,7 +480,8 @@ __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t 
     const int h = int(wid % ng) * HPW + lane / LPH;
     if (h >= a.H) return;
     const int64_t run = (wid / ng) % nruns, brow = wid / ng / nruns;
-    const int64_t t0 = run * a.run, t1 = t0 + a.run < a.T ? t0 + a.run : a.T;
+    int t0, t1;
+    owned_tokens(a, run, t0, t1);
     const int64_t stride = int64_t(a.H) * D, row0 = brow * a.T * stride;
     const int chan = h * D + (lane % LPH) * 8;
     const T* logit = static_cast<const T*>(a.logit[WHICH]) + row0;
@@ -578,19 +592,23 @@ int64_t epilogue_bwd_partials(int64_t rows, int32_t dv)
 }
 
 // Long runs repeat few tokens at their ends and leave few partial rows; short ones
-// give a small call enough wavefronts.  So: the longest of 32, 16, 8 (and, for
-// short filters, 4) steps that leaves kWantWaves convolution wavefronts.  5003
-// packed tokens of 6 heads: 41 us with four steps, 37 with eight; 4096 tokens of 16
-// heads: 82 us with eight, 75 with sixteen.  The length is such that a run and the
-// K - 1 tokens after it are whole steps.
+// give a small call enough wavefronts, and a large one several rounds of the 2048
+// that are resident.  So: the longest of 32, 16, 8 (and, for short filters, 4)
+// steps that leaves a thousand convolution wavefronts, 32 only with four thousand
+// (four taps; longer filters pay more for a run's end).  5003 packed tokens of 6
+// heads: 41 us with four steps, 37 with eight; 4096 tokens of 16 heads: 82 us with
+// eight, 75 with sixteen; 4 x 4096 FP32 tokens of 16 heads: 462 us with 32, 428 with
+// sixteen.  The length is such that a run and the K - 1 tokens after it are whole
+// steps.
 int32_t prologue_bwd_run(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t K)
 {
     const int cpl = channels_per_lane(K), d = dk < dv ? dk : dv, hpw = 64 / (d / cpl);
     const int64_t per_run = 3 * int64_t(B) * ((H + hpw - 1) / hpw);  // convolution wavefronts
+    const auto length = [K](int32_t steps) { return steps * kStep - (K - 1); };
+    const auto waves = [&](int32_t steps) { return per_run * ((int64_t(T) + length(steps) - 1) / length(steps)); };
     int32_t steps = 32;
-    while (steps > (K <= 4 ? 4 : 8) && per_run * ((int64_t(T) + steps * kStep - K) / (steps * kStep - (K - 1))) < kWantWaves)
-        steps /= 2;
-    return steps * kStep - (K - 1);
+    while (steps > (K <= 4 ? 4 : 8) && waves(steps) < (steps == 32 && K <= 4 ? 4096 : 1024)) steps /= 2;
+    return length(steps);
 }
 
 hipError_t launch_mixer_epilogue_bwd(const EpilogueBwdArgs& a, bool bf16, hipStream_t stream)

@@ -506,6 +506,9 @@ size_t gdn2_mixer_epilogue_bwd_workspace_bytes(int64_t rows, int32_t dv);
  *              wanted.
  *   d_conv_state_in : like d_conv_state_out, or NULL if not wanted (it exists
  *              also where conv_state_in was NULL: the gradient at zero).
+ *   Packed input may end in padding here: tokens from cu_seqlens[num_seqs] on (and
+ *              before cu_seqlens[0]) are not read, and their gradients stay as
+ *              they were.
  *   workspace: gdn2_mixer_prologue_bwd_workspace_bytes bytes of device memory,
  *              16-byte aligned, when a filter's gradient is wanted (else it may be
  *              NULL).  Missing or smaller: GDN2_ERR_WORKSPACE.

@@ -527,6 +527,40 @@ def test_prologue_bwd_unwanted_and_repeated():
         assert c[n] is None if "conv" in n else torch.equal(a[n], c[n]), n
 
 
+@pytest.mark.parametrize("K", [1, 4, 7])
+def test_prologue_bwd_padding_is_left_alone(K):
+    """Packed sequences in a longer buffer with NaN behind them: the gradients are those of the sequences alone, and the
+    gradient buffers keep what they held there."""
+    import torch
+
+    lens, pad = [5, 0, 130, 33], 77
+    p = Prologue(713, 1, 0, 3, 64, 32, K, "bf16", lens=lens)
+    ref = p.run()
+    T, padded = sum(lens), []
+    for z in p.t:
+        if z.dim() == 4:
+            z = torch.cat([z, torch.full((1, pad, *z.shape[2:]), float("nan"), dtype=z.dtype, device="cuda")], 1)
+        padded.append(z)
+    out = {n: torch.full((1, T + pad, *ref[n].shape[2:]), 7.0, dtype=torch.bfloat16, device="cuda") if ref[n].dim() == 4
+           else torch.empty_like(ref[n]) for n in ref}
+    ws = torch.empty(binding.gdn2_mixer_prologue_bwd_workspace_bytes(1, T + pad, 3, 64, 32, K), dtype=torch.uint8, device="cuda")
+    at = lambda z: z.data_ptr()  # noqa: E731
+    rc = binding.load().gdn2_mixer_prologue_bwd(
+        *map(at, padded[:8]), at(p.how["conv_state"]), *map(at, padded[8:]), at(p.how["d_conv_state_out"]),
+        *map(at, out.values()), at(p.how["cu_seqlens"]), 1, T + pad, 3, 64, 32, K, len(lens), 0.125, 1e-6, 1, at(ws),
+        ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0
+    for n, want in ref.items():
+        if want.dim() == 4:
+            assert torch.equal(out[n][:, :T], want), n
+            assert (out[n][:, T:] == 7).all(), n
+        elif "state" in n:
+            assert torch.equal(out[n], want), n
+        else:  # summed over another partition of the tokens
+            assert torch.isfinite(out[n]).all() and (out[n] - want).norm() <= T * O.U * want.abs().max() * want.numel() ** 0.5, n
+
+
 def test_prologue_bwd_malformed_offsets_stay_inside():
     """Offsets out of order or out of range are clamped like the forward call's: the call ends without a fault and the
     inputs are as they were (the results mean nothing); a well-formed call after it is right."""
