@@ -443,6 +443,45 @@ def bench_mixer(args):
     return rows
 
 
+def bench_training(args):
+    """The training operators on batched_bf16's shape (B=8, T=4096, H=16, d=128,
+    bf16; 2048 channels a token): one report row each."""
+    import torch
+
+    from delta_rule_linear_gdn2_amd import binding
+
+    B, T, H, d, K = 8, 4096, 16, 128, 4
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def new(*shape, dtype=torch.bfloat16):
+        return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+
+    tokens = [new(B, T, H, d) for _ in range(10)]
+    conv = [0.5 * new(H * d, K, dtype=torch.float32) for _ in range(3)]
+    wgt = torch.ones(d, dtype=torch.float32, device="cuda")
+    x, u, gate, dx, dh = (z.view(B, T, H * d) for z in tokens[:5])
+    w = torch.ones(H * d, dtype=torch.float32, device="cuda")
+    step = dict(gate=gate, gate_layout="full", weight_post=w, weight_pre=w, residual_scale=0.5, dropout_p=0.1, seed=3)
+    n = B * T * H * d
+    calls = (("block step (gdn2_block_norm_fwd)", 10 * n, lambda: binding.gdn2_block_norm_fwd(x, u, **step)),
+             ("block step backward (gdn2_block_norm_bwd)", 16 * n,
+              lambda: binding.gdn2_block_norm_bwd(x, u, dx, dh, **step)),
+             ("dropout (gdn2_dropout)", 4 * n, lambda: binding.gdn2_dropout(x, 0.1, 3)),
+             ("token-mixer epilogue backward", 10 * n,
+              lambda: binding.gdn2_mixer_epilogue_bwd(tokens[0], tokens[1], wgt, tokens[2])),
+             ("token-mixer prologue backward (K=4)", 30 * n,
+              lambda: binding.gdn2_mixer_prologue_bwd(*tokens[:3], *conv, *tokens[3:10], q_scale=d ** -0.5)))
+    rows = []
+    for name, nbytes, call in calls:
+        per, _, _ = time_events(call, args.warmup, args.steps)
+        ms = float(np.median(per))
+        log(f"{name}: {ms * 1e3:.1f} us, {nbytes / (ms / 1e3) / 1e9:.0f} GB/s")
+        rows.append({"report": "config", "workload": f"batched_bf16 {name}", "us_per_call": ms * 1e3,
+                     "GBps": nbytes / (ms / 1e3) / 1e9, "hbm_frac": nbytes / (ms / 1e3) / 1e9 / HBM_PEAK_GBPS,
+                     "algorithmic_bytes": nbytes})
+    return rows
+
+
 def run_only(args):
     """One part alone (for rocprofv3 runs); prints one JSON line."""
     import torch
@@ -465,6 +504,8 @@ def run_only(args):
                "median_launch_ms": float(np.median(ch["per"])), "launches": args.steps + args.warmup}
     elif args.only == "mixer":
         res = {"part": "mixer", "rows": bench_mixer(args), "launches": args.steps + args.warmup}
+    elif args.only == "training":
+        res = {"part": "training", "rows": bench_training(args), "launches": args.steps + args.warmup}
     else:
         nbytes = 1 << 30
         src = torch.empty(nbytes // 4, dtype=torch.float32, device="cuda").fill_(1.0)
@@ -590,6 +631,9 @@ def run_configs(args):
     # the token mixer around the recurrence on the headline shape (HBM-bound passes)
     for row in bench_mixer(args):
         print(json.dumps(row), flush=True)
+    # the training operators around it
+    for row in bench_training(args):
+        print(json.dumps(row), flush=True)
     # the gate-aware backward on the headline shape, and the oracle's reverse mode beside it
     bw = bench_bwd(args)
     t0 = time.perf_counter()
@@ -650,7 +694,7 @@ def main():
                     help="untimed chunkwise launches before the warm-up ones, so that the timed launches run on a "
                          "settled shader clock (headline line and --configs; --only parts take none)")
     ap.add_argument("--no-decode", action="store_true", help="skip the decode half")
-    ap.add_argument("--only", choices=["chunk", "decode", "copy", "bwd", "mixer", "segmented"], default=None,
+    ap.add_argument("--only", choices=["chunk", "decode", "copy", "bwd", "mixer", "training", "segmented"], default=None,
                     help="profiling aid: run one part only and print its timing line "
                          "(copy = a plain 1 GiB device copy, the reference for HBM byte counters; "
                          "segmented = layer_bf16 through the few-chain segmented path)")
