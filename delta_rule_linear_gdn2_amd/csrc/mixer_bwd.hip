@@ -24,9 +24,9 @@
 // gradients.  An input's gradient needs the K - 1 tokens after it, so a run reads
 // that many tokens past its end (and before its start).  The filters' gradients of
 // a run go to the workspace and are added by the column-sum kernel.  B=8, T=4096,
-// H=16, d=128, K=4, bf16: 426 us a call; the kernel's 415 us move 2.07 GB, 1.03
+// H=16, d=128, K=4, bf16: 424 us a call; the kernel's 416 us move 2.07 GB, 1.03
 // times inputs and outputs, with 61% of the vector issue slots taken beside.
-// Outputs are written past the caches (426 us; 432 through them).
+// Outputs are written past the caches (2% less time than through them).
 #include <type_traits>
 
 #include "row_device.hpp"
