@@ -368,6 +368,23 @@ def test_calls_at_once_on_two_streams():
             assert torch.equal(g[name], v), name
 
 
+@pytest.mark.parametrize("dtype,res", TYPES)
+def test_fused_step_is_the_step_and_then_the_norm(dtype, res):
+    """The norm of the stored stream alone gives the fused call's h, bit for bit, and so do its gradients in turn."""
+    import torch
+
+    for D in (75, 96, 1371, 2048):
+        b = Block(549 + D, 40, D, dtype, res, "full", "silu", p=0.2)
+        x_out, h = b.fwd()
+        t = b.t["u"].dtype
+        assert torch.equal(binding.gdn2_block_norm_fwd(x_out, weight_pre=b.t["w_pre"], dtype=t)[1], h)
+        alone, _ = b.fwd(weight_pre=None)
+        assert torch.equal(alone, x_out)
+        fused = b.bwd(x_out)
+        norm = binding.gdn2_block_norm_bwd(x_out, None, b.t["d_x_out"], b.t["d_h"], weight_pre=b.t["w_pre"])
+        assert torch.equal(norm["d_x"], fused["d_x"])
+
+
 def test_one_leading_axis_or_several():
     """A call over [B, T, D] is the call over its rows."""
     import torch
