@@ -11,6 +11,10 @@
 // second set of registers.  Two sums over the row, one barrier each where it
 // spans wavefronts.  The weights' column sums stay in registers over all rows of
 // a workgroup.
+//
+// A norm's gradient is taken as (w dh - x (mean(w dh x) / rms / rms)) / rms, 1 / rms
+// going in factor by factor: its cube leaves the FP32 range for rows past 1e12 (and
+// below 1e-12, with an eps as small) though the gradient does not.
 #include "block_device.hpp"
 
 namespace gdn2 {
@@ -136,7 +140,7 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
         }
         if (pre || post) row_sums<LPR, WPR, 3>(s, lds, turn);
         const float rx = __builtin_amdgcn_rsqf(fmaf(s[0], inv_d, a.eps));
-        const float back_x = rx * rx * rx * s[1] * inv_d;
+        const float back_x = rx * (rx * s[1] * inv_d);
         const float ru = post ? __builtin_amdgcn_rsqf(fmaf(s[2], inv_d, a.eps)) : 1.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -152,9 +156,8 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
                 dh[i].get(hv);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float hr = hv[j] * rx;
-                    acc_pre[i][j] = fmaf(hr, xv[j], acc_pre[i][j]);
-                    t[i][j] = fmaf(hr, wr[i][j], fmaf(-back_x, xv[j], t[i][j]));
+                    acc_pre[i][j] = fmaf(hv[j] * rx, xv[j], acc_pre[i][j]);
+                    t[i][j] = fmaf(rx, fmaf(-back_x, xv[j], wr[i][j] * hv[j]), t[i][j]);
                 }
             }
             Eight<R> out;
@@ -225,14 +228,14 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
         }
         if (post || token_gate) row_sums<LPR, WPR, 2>(q, lds, turn);
         if (token_gate && a.d_gate && rl == 0 && live) store_from_f32(static_cast<T*>(a.d_gate), row, dta * q[1]);
-        const float back_u = ru * ru * ru * q[0] * inv_d;
+        const float back_u = ru * (ru * q[0] * inv_d);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if (post) {
                 float uv[8];
                 u[i].get(uv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) t[i][j] = fmaf(ru, t[i][j], -back_u * uv[j]);
+                for (int j = 0; j < 8; ++j) t[i][j] = ru * fmaf(-back_u, uv[j], t[i][j]);
             }
             Eight<T> out;
             out.put(t[i]);

@@ -14,7 +14,8 @@
 // and db_logit = db b (1 - b).  The gradients at the K - 1 positions before a
 // sequence are the carried state's; the gradient of the state after a sequence
 // belongs to its last K - 1 inputs.  y, the activations and the norms are
-// remade from the inputs; all arithmetic is FP32.
+// remade from the inputs; all arithmetic is FP32, with 1 / rms and r going in factor by
+// factor (their cubes leave its range before the gradients do).
 //
 // HBM-bound, one pass.  Epilogue: dv / 8 lanes a row, eight channels a lane, the
 // weight's gradient in registers over many rows (524288 rows of 128 bf16: 130 us
@@ -81,12 +82,12 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
         ss = group_sum<G>(ss);
         so = group_sum<G>(so);
         const float rr = __builtin_amdgcn_rsqf(ss * (1.0f / DV) + a.eps);
-        const float back = rr * rr * rr * so * (1.0f / DV);
+        const float back = rr * (rr * so * (1.0f / DV));
         float d[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             acc[j] = fmaf(dn[j], o[j] * rr, acc[j]);
-            d[j] = rr * w[j] * dn[j] - o[j] * back;
+            d[j] = rr * fmaf(-o[j], back, w[j] * dn[j]);
             dg[j] *= rr;
         }
         Eight<T> out;
@@ -344,15 +345,12 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
             ss = group_sum<LPH>(ss);
             sv = group_sum<LPH>(sv);
             r = __builtin_amdgcn_rsqf(ss + a.eps_l2);
-            back = r * r * r * sv;
-            if (PATH == 0) {
-                r *= a.q_scale;
-                back *= a.q_scale;
-            }
+            back = r * (r * sv);
+            if (PATH == 0) r *= a.q_scale;
         }
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            dy[c] *= PATH < 2 ? r * g[c] - v[c] * back : g[c];
+            dy[c] *= PATH < 2 ? r * fmaf(-v[c], back, g[c]) : g[c];
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 if (j >= low) pend[i + j][c] = fmaf(w[j][c], dy[c], pend[i + j][c]);

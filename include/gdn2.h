@@ -424,7 +424,8 @@ typedef enum gdn2_block_gate {
  *   stream: GDN2_ERR_BAD_DTYPE).  1 <= D <= 16384 (above: GDN2_ERR_UNSUPPORTED),
  *   any D, at full speed for multiples of 8.  rows >= 0.  eps > 0.
  * Outputs must not overlap inputs (but x_out = x) or each other.  The norms'
- * sums are FP32, so rows of entries past 1e19 overflow to a norm of zero.
+ * sums of D squares are FP32: a row whose sum passes 3e38 (entries of 1e19, or
+ * of 1e17 at D = 16384) overflows to a norm of zero.
  */
 gdn2_status gdn2_block_norm_fwd(const void* x, const void* u, const void* gate, const float* weight_post,
                                 const float* weight_pre, void* x_out, void* h, int64_t rows, int32_t D, float eps,
