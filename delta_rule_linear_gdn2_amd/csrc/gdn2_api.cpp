@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cstdint>
 #include <initializer_list>
+#include <limits>
 
 #include "gdn2.h"
 #include "launch.hpp"
@@ -363,6 +364,10 @@ bool misaligned(std::initializer_list<const void*> ptrs)
 
 constexpr int64_t kMaxRows = int64_t(1) << 40;  // byte counts of [rows, D] stay far inside 64 bits
 
+// The norms' eps of the training operators: a normal FP32 number.  A row of zeros takes
+// 1 / sqrt(eps), and the hardware's reciprocal square root of a subnormal number is infinity.
+bool eps_ok(float eps) { return eps >= std::numeric_limits<float>::min(); }
+
 // The dropout arguments, checked: p is a probability, the device offset aligned.
 gdn2_status dropout_args(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_device,
                          gdn2::DropoutArgs& d)
@@ -382,7 +387,7 @@ gdn2_status block_norm_check(bool has_u, const void* gate, const float* weight_p
 {
     if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
     if (rdtype != GDN2_DTYPE_F32 && rdtype != dtype) return GDN2_ERR_BAD_DTYPE;
-    if (rows < 0 || rows > kMaxRows || D <= 0 || !(eps > 0.f)) return GDN2_ERR_BAD_SHAPE;
+    if (rows < 0 || rows > kMaxRows || D <= 0 || !eps_ok(eps)) return GDN2_ERR_BAD_SHAPE;
     if (gate_layout < 0 || gate_layout > 3 || gate_act < 0 || gate_act > 2) return GDN2_ERR_BAD_SHAPE;
     if (D > gdn2::kBlockMaxD) return GDN2_ERR_UNSUPPORTED;
     if (gdn2_status s = dropout_args(p, seed, offset, offset_device, drop)) return s;
@@ -507,7 +512,7 @@ gdn2_status mixer_epilogue_bwd(const void* o, const void* gate, const float* wei
                                gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
-    if (rows < 0 || rows > kMaxRows || dv <= 0 || (act != 0 && act != 1) || !(eps > 0.f)) return GDN2_ERR_BAD_SHAPE;
+    if (rows < 0 || rows > kMaxRows || dv <= 0 || (act != 0 && act != 1) || !eps_ok(eps)) return GDN2_ERR_BAD_SHAPE;
     if (!supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
     if (rows > 0 && (!o || !gate || !weight || !d_y || !d_o || !d_gate)) return GDN2_ERR_NULL_POINTER;
     if (misaligned({o, gate, weight, d_y, d_o, d_gate, d_weight, workspace})) return GDN2_ERR_MISALIGNED;

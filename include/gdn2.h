@@ -422,7 +422,8 @@ typedef enum gdn2_block_gate {
  *   h        : [rows, D] dtype; NULL exactly when weight_pre is NULL.
  *   residual_dtype is dtype, or FP32 with bf16 blocks (FP32 blocks with a bf16
  *   stream: GDN2_ERR_BAD_DTYPE).  1 <= D <= 16384 (above: GDN2_ERR_UNSUPPORTED),
- *   any D, at full speed for multiples of 8.  rows >= 0.  eps > 0.
+ *   any D, at full speed for multiples of 8.  rows >= 0.  eps >= 2^-126 (a normal
+ *   FP32 number: a row of zeros takes 1 / sqrt(eps); below: GDN2_ERR_BAD_SHAPE).
  * Outputs must not overlap inputs (but x_out = x) or each other.  The norms'
  * sums of D squares are FP32: a row whose sum passes 3e38 (entries of 1e19, or
  * of 1e17 at D = 16384) overflows to a norm of zero.
@@ -479,7 +480,8 @@ gdn2_status gdn2_dropout(const void* x, void* y, int64_t rows, int64_t D, double
 
 /*
  * Gradients of gdn2_mixer_epilogue for the loss <d_y, y>.
- *   o, gate, weight, rows, dv, eps, gate_act, dtype: the forward call's.
+ *   o, gate, weight, rows, dv, eps, gate_act, dtype: the forward call's (eps at
+ *   least 2^-126; below: GDN2_ERR_BAD_SHAPE).
  *   d_y, d_o, d_gate : [rows, dv] dtype.   d_weight : [dv] FP32, or NULL if not
  *   wanted; with it a workspace of gdn2_mixer_epilogue_bwd_workspace_bytes bytes,
  *   16-byte aligned (missing or smaller: GDN2_ERR_WORKSPACE).
