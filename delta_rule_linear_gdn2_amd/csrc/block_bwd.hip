@@ -179,15 +179,10 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
         float q[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            // c = scale * m * t, nothing behind the row's end
+            // scale * t, nothing behind the row's end; the gate's part of its gradient, c n
 #pragma unroll
             for (int j = 0; j < 8; ++j) t[i][j] = grp[i].has(j, a.D, live) ? factor * t[i][j] : 0.f;
-            if (a.drop.threshold) {
-                const u32x4_t bits = philox4x32(uint64_t(row * groups + grp[i].col / 8), offset, a.drop.seed);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) t[i][j] = philox_keep(bits, j, a.drop.threshold) ? t[i][j] : 0.f;
-            }
-            float uv[8], hat[8];
+            float uv[8], hat[8], dg[8];
             u[i].get(uv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) hat[j] = uv[j] * ru;
@@ -196,26 +191,39 @@ __global__ __launch_bounds__((Cover<LPR, WPR, NI>::kThreads), (bwd_waves_per_sim
                 g[i].get(gv);
                 act_values(a.act, gv, f, df);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) df[j] *= t[i][j] * (hat[j] * wp[i][j]);
+                for (int j = 0; j < 8; ++j) dg[j] = df[j] * (t[i][j] * (hat[j] * wp[i][j]));
 #pragma unroll
                 for (int j = 0; j < 8; ++j) t[i][j] *= f[j];
+            } else if (CHANNEL || token_gate) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    dg[j] = t[i][j] * (hat[j] * wp[i][j]);
+                    t[i][j] *= CHANNEL ? ch[i][j] : ta;
+                }
+            }
+            // the mask comes after the products: what a dropped element holds, NaN and
+            // infinity too, reaches neither gradient
+            if (a.drop.threshold) {
+                const u32x4_t bits = philox4x32(uint64_t(row * groups + grp[i].col / 8), offset, a.drop.seed);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool keep = philox_keep(bits, j, a.drop.threshold);
+                    t[i][j] = keep ? t[i][j] : 0.f;
+                    dg[j] = keep ? dg[j] : 0.f;
+                }
+            }
+            if (full_gate) {
                 if (a.d_gate) {
                     Eight<T> out;
-                    out.put(df);
+                    out.put(dg);
                     grp[i].store(out, static_cast<T*>(a.d_gate) + row * a.D, a.D, live);
                 }
             } else if (CHANNEL) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    acc_gate[i][j] = fmaf(t[i][j], hat[j] * wp[i][j], acc_gate[i][j]);
-                    t[i][j] *= ch[i][j];
-                }
+                for (int j = 0; j < 8; ++j) acc_gate[i][j] += dg[j];
             } else if (token_gate) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    q[1] = fmaf(t[i][j], hat[j] * wp[i][j], q[1]);
-                    t[i][j] *= ta;
-                }
+                for (int j = 0; j < 8; ++j) q[1] += dg[j];
             }
             if (post) {
 #pragma unroll

@@ -453,7 +453,9 @@ gdn2_status gdn2_block_norm_fwd(const void* x, const void* u, const void* gate, 
  *              CHANNEL d_gate is wanted (else it may be NULL); contents on entry
  *              do not matter.  Missing or smaller: GDN2_ERR_WORKSPACE.
  * The gradient of a shared input is the sum over all that share it (zero when
- * rows = 0).  Outputs and the workspace must not overlap inputs (but d_x =
+ * rows = 0).  What u and the gate hold at a dropped element, NaN and infinity too,
+ * reaches no gradient (a u of NaN or infinity under weight_post is in its row's
+ * norm, and so in the row).  Outputs and the workspace must not overlap inputs (but d_x =
  * d_x_out) or each other.  Calls that may run at the same time need a workspace
  * each.
  */
