@@ -31,6 +31,7 @@ EXPORTS = ("gdn2_block_norm_bwd", "gdn2_block_norm_bwd_workspace_bytes", "gdn2_b
            "gdn2_chunk_fwd_workspace_bytes", "gdn2_dropout",
            "gdn2_mixer_epilogue", "gdn2_mixer_epilogue_bwd", "gdn2_mixer_epilogue_bwd_workspace_bytes",
            "gdn2_mixer_prologue", "gdn2_mixer_prologue_bwd", "gdn2_mixer_prologue_bwd_workspace_bytes",
+           "gdn2_mixer_prologue_bwd_zeroed",
            "gdn2_recurrent_fwd", "gdn2_recurrent_step",
            "gdn2_recurrent_step_gates", "gdn2_status_string", "gdn2_version")
 
@@ -113,8 +114,9 @@ def load(path: str = LIB_PATH):
     lib.gdn2_mixer_epilogue_bwd.restype = ctypes.c_int
     lib.gdn2_mixer_epilogue_bwd_workspace_bytes.argtypes = [L, I]
     lib.gdn2_mixer_epilogue_bwd_workspace_bytes.restype = Z
-    lib.gdn2_mixer_prologue_bwd.argtypes = [P] * 25 + [I] * 7 + [F, F, I, P, Z, P]
-    lib.gdn2_mixer_prologue_bwd.restype = ctypes.c_int
+    for f in (lib.gdn2_mixer_prologue_bwd, lib.gdn2_mixer_prologue_bwd_zeroed):
+        f.argtypes = [P] * 25 + [I] * 7 + [F, F, I, P, Z, P]
+        f.restype = ctypes.c_int
     lib.gdn2_mixer_prologue_bwd_workspace_bytes.argtypes = [I] * 6
     lib.gdn2_mixer_prologue_bwd_workspace_bytes.restype = Z
     lib.gdn2_status_string.argtypes = [ctypes.c_int]
@@ -808,8 +810,9 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
     d_q, d_k, d_b: [B, T, H, dk] and d_v, d_w: [B, T, H, dv] of the inputs' type;
     d_conv_state_out: [N, H * (2 dk + dv), K - 1] float32 or None.  Returns
     dict(d_xq, d_xk, d_xv, d_conv_q, d_conv_k, d_conv_v, d_b_logit, d_w_logit,
-    d_conv_state), None in the place of what is not wanted.  ``workspace``
-    (uint8) is allocated when not given.
+    d_conv_state), None in the place of what is not wanted.  Packed input may be
+    longer than its sequences: tokens that none of them owns are not read, and
+    their gradients are zero.  ``workspace`` (uint8) is allocated when not given.
     """
     key, value, index, dt = xq.shape, xv.shape, xq.get_device(), xq.dtype
     if len(key) != 4 or len(value) != 4:
@@ -838,7 +841,7 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
     out["d_conv_state"] = conv_q.new_empty(st_shape) if output_d_conv_state else None
     need = gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, dk, dv, K) if want_d_conv else 0
     workspace, ws_bytes = _workspace(workspace, need, xq)
-    _run("gdn2_mixer_prologue_bwd", index, xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), conv_q.data_ptr(),
+    _run("gdn2_mixer_prologue_bwd_zeroed", index, xq.data_ptr(), xk.data_ptr(), xv.data_ptr(), conv_q.data_ptr(),
          conv_k.data_ptr(), conv_v.data_ptr(), b_logit.data_ptr(), w_logit.data_ptr(), _addr(conv_state),
          d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), d_b.data_ptr(), d_w.data_ptr(), _addr(d_conv_state_out),
          *[_addr(t) for t in out.values()], _addr(cu_seqlens), B, T, H, dk, dv, K, N, q_scale, eps_l2, code,

@@ -542,8 +542,8 @@ gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&c
                                const void* const (&d_gate)[2], const float* d_state_out, void* const (&d_x)[3],
                                float* const (&d_conv)[3], void* const (&d_logit)[2], float* d_state_in,
                                const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
-                               int32_t K, int32_t num_seqs, float q_scale, float eps_l2, gdn2_dtype dtype,
-                               void* workspace, size_t workspace_bytes, void* stream)
+                               int32_t K, int32_t num_seqs, float q_scale, float eps_l2, bool zero_padding,
+                               gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
     if (B <= 0 || T < 0 || H <= 0 || dk <= 0 || dv <= 0 || K < 1 || K > 16) return GDN2_ERR_BAD_SHAPE;
@@ -599,6 +599,7 @@ gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&c
     a.cu_seqlens = cu_seqlens;
     a.B = B, a.T = T, a.H = H, a.dk = dk, a.dv = dv, a.K = K, a.N = N;
     a.q_scale = q_scale, a.eps_l2 = eps_l2;
+    a.zero_padding = zero_padding;
     a.run = gdn2::prologue_bwd_run(B, T, H, dk, dv, K);
     a.partial = need ? static_cast<float*>(workspace) : nullptr;
     const hipError_t e = gdn2::launch_mixer_prologue_bwd(a, dtype == GDN2_DTYPE_BF16, static_cast<hipStream_t>(stream));
@@ -919,8 +920,26 @@ gdn2_status gdn2_mixer_prologue_bwd(const void* xq, const void* xk, const void* 
     return mixer_prologue_bwd({xq, xk, xv}, {conv_q, conv_k, conv_v}, {b_logit, w_logit}, conv_state_in,
                               {d_q, d_k, d_v}, {d_b, d_w}, d_conv_state_out, {d_xq, d_xk, d_xv},
                               {d_conv_q, d_conv_k, d_conv_v}, {d_b_logit, d_w_logit}, d_conv_state_in, cu_seqlens, B,
-                              T, H, dk, dv, kernel_size, num_seqs, q_scale, eps_l2, dtype, workspace, workspace_bytes,
-                              stream);
+                              T, H, dk, dv, kernel_size, num_seqs, q_scale, eps_l2, false, dtype, workspace,
+                              workspace_bytes, stream);
+}
+
+gdn2_status gdn2_mixer_prologue_bwd_zeroed(const void* xq, const void* xk, const void* xv, const float* conv_q,
+                                           const float* conv_k, const float* conv_v, const void* b_logit,
+                                           const void* w_logit, const float* conv_state_in, const void* d_q,
+                                           const void* d_k, const void* d_v, const void* d_b, const void* d_w,
+                                           const float* d_conv_state_out, void* d_xq, void* d_xk, void* d_xv,
+                                           float* d_conv_q, float* d_conv_k, float* d_conv_v, void* d_b_logit,
+                                           void* d_w_logit, float* d_conv_state_in, const int32_t* cu_seqlens,
+                                           int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
+                                           int32_t kernel_size, int32_t num_seqs, float q_scale, float eps_l2,
+                                           gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return mixer_prologue_bwd({xq, xk, xv}, {conv_q, conv_k, conv_v}, {b_logit, w_logit}, conv_state_in,
+                              {d_q, d_k, d_v}, {d_b, d_w}, d_conv_state_out, {d_xq, d_xk, d_xv},
+                              {d_conv_q, d_conv_k, d_conv_v}, {d_b_logit, d_w_logit}, d_conv_state_in, cu_seqlens, B,
+                              T, H, dk, dv, kernel_size, num_seqs, q_scale, eps_l2, true, dtype, workspace,
+                              workspace_bytes, stream);
 }
 
 size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,

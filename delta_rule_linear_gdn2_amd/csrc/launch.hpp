@@ -231,6 +231,7 @@ struct PrologueBwdArgs {
     const int32_t* cu_seqlens;
     int32_t B, T, H, dk, dv, K, N;
     float q_scale, eps_l2;
+    bool zero_padding;        // write zeros to the gradients of tokens that no sequence owns
     int32_t run;              // tokens per wavefront
     float* partial;           // [B * ceil(T / run)][H * (2 dk + dv) * K], or null when no filter gradient is wanted
 };

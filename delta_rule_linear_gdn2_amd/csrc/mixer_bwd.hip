@@ -151,7 +151,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int32_t T, 
 }
 
 // Tokens [t0, t1) of run `run` that some sequence owns (packed input may end in
-// padding, which is neither read nor written); t1 <= t0: none.
+// padding, which is not read and, but for padding_path, not written); t1 <= t0:
+// none.
 __device__ __forceinline__ void owned_tokens(const PrologueBwdArgs& a, int64_t run, int& t0, int& t1)
 {
     t0 = int(run * a.run);
@@ -513,6 +514,7 @@ __device__ __forceinline__ void gate_bwd_path(const PrologueBwdArgs& a, int64_t 
 // Sequences without tokens carry their state through, and its gradient back.
 __device__ __forceinline__ void empty_sequences_path(const PrologueBwdArgs& a)
 {
+    if (!a.d_state_in || a.K == 1) return;
     const int64_t per = int64_t(a.H) * (2 * a.dk + a.dv) * (a.K - 1), total = int64_t(a.N) * per;
     for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += int64_t(gridDim.x) * kThreads) {
         int64_t bos, eos, brow;
@@ -521,7 +523,27 @@ __device__ __forceinline__ void empty_sequences_path(const PrologueBwdArgs& a)
     }
 }
 
-// blockIdx.y: 0 q, 1 k, 2 v, 3 b, 4 w, 5 the empty sequences.  The head width is
+// Zeros to the gradients of the tokens in front of the first sequence and behind the
+// last, where the call asks for them: two ranges of each buffer.
+template <typename T>
+__device__ __forceinline__ void padding_path(const PrologueBwdArgs& a)
+{
+    if (!a.cu_seqlens || !a.zero_padding) return;
+    const int first = a.cu_seqlens[0], end = a.cu_seqlens[a.N];
+    const int64_t lead = first < 0 ? 0 : first < a.T ? first : a.T, tail = a.T - (end < 0 ? 0 : end < a.T ? end : a.T);
+    if (lead == 0 && tail == 0) return;
+    const Eight<T> zero = {};
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        T* out = static_cast<T*>(i < 3 ? a.d_x[i] : a.d_logit[i - 3]);
+        const int64_t per = int64_t(a.H) * (i == 2 || i == 4 ? a.dv : a.dk) / 8;  // groups of eight a token
+        const int64_t skip = (a.T - tail - lead) * per, total = (lead + tail) * per;
+        for (int64_t g = int64_t(blockIdx.x) * kThreads + threadIdx.x; g < total; g += int64_t(gridDim.x) * kThreads)
+            zero.store(out + (g < lead * per ? g : g + skip) * 8);
+    }
+}
+
+// blockIdx.y: 0 q, 1 k, 2 v, 3 b, 4 w, 5 the empty sequences and the padding.  The head width is
 // looked up here, so a call is one launch whether or not dk = dv.
 template <typename T, int KM>
 __global__ __launch_bounds__(kThreads) void prologue_bwd_kernel(PrologueBwdArgs a)
@@ -545,7 +567,7 @@ __global__ __launch_bounds__(kThreads) void prologue_bwd_kernel(PrologueBwdArgs 
         case 1024 + 32: gate_bwd_path<T, 32, 1>(a, wid, lane); break;
         case 1024 + 64: gate_bwd_path<T, 64, 1>(a, wid, lane); break;
         case 1024 + 128: gate_bwd_path<T, 128, 1>(a, wid, lane); break;
-        default: empty_sequences_path(a); break;
+        default: empty_sequences_path(a); padding_path<T>(a); break;
     }
 }
 
@@ -553,12 +575,13 @@ template <typename T>
 hipError_t prologue_typed(const PrologueBwdArgs& a, hipStream_t stream)
 {
     const bool empties = a.d_state_in && a.K > 1 && (a.cu_seqlens || a.T == 0);
+    const bool rest = empties || (a.cu_seqlens && a.zero_padding);
     if (a.T > 0 || empties) {
         const int d = a.dk > a.dv ? a.dk : a.dv, hpw = 64 / (d / channels_per_lane(a.K));
         const int64_t waves = int64_t(a.B) * ((int64_t(a.T) + a.run - 1) / a.run) * ((a.H + hpw - 1) / hpw);
         const int64_t blocks = waves > 0 ? (waves + 3) / 4 : 1;
         if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-        const dim3 grid{unsigned(blocks), empties ? 6u : 5u, 1}, block{kThreads, 1, 1};
+        const dim3 grid{unsigned(blocks), rest ? 6u : 5u, 1}, block{kThreads, 1, 1};
 #define GDN2_TAPS(KM) hipLaunchKernelGGL((prologue_bwd_kernel<T, KM>), grid, block, 0, stream, a)
         switch (a.K) {
             case 1: GDN2_TAPS(1); break;

@@ -511,9 +511,10 @@ size_t gdn2_mixer_epilogue_bwd_workspace_bytes(int64_t rows, int32_t dv);
  *              wanted.
  *   d_conv_state_in : like d_conv_state_out, or NULL if not wanted (it exists
  *              also where conv_state_in was NULL: the gradient at zero).
- *   Packed input may end in padding here: tokens from cu_seqlens[num_seqs] on (and
- *              before cu_seqlens[0]) are not read, and their gradients stay as
- *              they were.
+ *   Packed input may end in padding here, though the forward call's ends at T (its
+ *              outputs in padding mean nothing): tokens from cu_seqlens[num_seqs] on
+ *              (and before cu_seqlens[0]) are not read, and their gradients stay as
+ *              they were.  gdn2_mixer_prologue_bwd_zeroed sets those to zero.
  *   workspace: gdn2_mixer_prologue_bwd_workspace_bytes bytes of device memory,
  *              16-byte aligned, when a filter's gradient is wanted (else it may be
  *              NULL).  Missing or smaller: GDN2_ERR_WORKSPACE.
@@ -528,6 +529,20 @@ gdn2_status gdn2_mixer_prologue_bwd(const void* xq, const void* xk, const void* 
                                     const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t dk,
                                     int32_t dv, int32_t kernel_size, int32_t num_seqs, float q_scale, float eps_l2,
                                     gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* gdn2_mixer_prologue_bwd for gradient buffers that hold nothing yet: the same in
+ * every argument, check and result, but that the gradients of tokens which no
+ * sequence owns are written too, as the zeros that they are. */
+gdn2_status gdn2_mixer_prologue_bwd_zeroed(const void* xq, const void* xk, const void* xv, const float* conv_q,
+                                           const float* conv_k, const float* conv_v, const void* b_logit,
+                                           const void* w_logit, const float* conv_state_in, const void* d_q,
+                                           const void* d_k, const void* d_v, const void* d_b, const void* d_w,
+                                           const float* d_conv_state_out, void* d_xq, void* d_xk, void* d_xv,
+                                           float* d_conv_q, float* d_conv_k, float* d_conv_v, void* d_b_logit,
+                                           void* d_w_logit, float* d_conv_state_in, const int32_t* cu_seqlens,
+                                           int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
+                                           int32_t kernel_size, int32_t num_seqs, float q_scale, float eps_l2,
+                                           gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace of gdn2_mixer_prologue_bwd: one partial row of H x (2 dk + dv) x K
  * FP32 sums per run of tokens of a batch row, rounded up to 256 bytes.  0 for
