@@ -351,7 +351,7 @@ __device__ __forceinline__ void conv_bwd_path(const PrologueBwdArgs& a, int64_t 
         }
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            dy[c] *= PATH < 2 ? r * fmaf(-v[c], back, g[c]) : g[c];
+            dy[c] = PATH < 2 ? (dy[c] * r) * fmaf(-v[c], back, g[c]) : dy[c] * g[c];  // products side by side
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 if (j >= low) pend[i + j][c] = fmaf(w[j][c], dy[c], pend[i + j][c]);
