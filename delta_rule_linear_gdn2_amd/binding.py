@@ -527,9 +527,9 @@ def _import_torch():
     global torch
     import torch as module
 
-    torch = module
-    _CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
     load()
+    _CODES.update({module.float32: DTYPE_F32, module.bfloat16: DTYPE_BF16})
+    torch = module  # last: from here on calls take the rest as done
 
 
 def _code(dt):
