@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -542,24 +543,32 @@ def _on_stream(f):
     workspace) belongs to that stream, and the caller's tensors are recorded on
     it: memory that one stream still uses is never handed to another."""
 
+    signature = inspect.signature(f)
+    name = next(iter(signature.parameters))
+
     @functools.wraps(f)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if torch is None:
             _import_torch()
+        first = args[0] if args else kw.get(name)
+        if first is None:
+            return f(*args, **kw)  # raises
         if stream is not None:
             if stream.device != first.device:
                 raise ValueError(f"stream: on {stream.device}, the tensors are on {first.device}")
-            for t in (first, *args, *kw.values()):
+            for t in (*args, *kw.values()):
                 if isinstance(t, torch.Tensor) and t.is_cuda:
                     t.record_stream(stream)
             with torch.cuda.stream(stream):
-                return f(first, *args, **kw)
+                return f(*args, **kw)
         index = first.get_device()
         if index >= 0 and index != torch.cuda.current_device():
             with torch.cuda.device(index):
-                return f(first, *args, **kw)
-        return f(first, *args, **kw)
+                return f(*args, **kw)
+        return f(*args, **kw)
 
+    parameters = [*signature.parameters.values(), inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)]
+    call.__signature__ = signature.replace(parameters=parameters)
     return call
 
 
