@@ -744,10 +744,10 @@ def gdn2_block_norm_bwd(x_out, u, d_x_out, d_h, *, gate=None, gate_layout="none"
         d_u = _buffer("d_u", d_u, u, shape, dt, index)
     elif d_u is not None:
         raise ValueError("d_u: there is none without u")
-    if gate is None or not want_d_gate:
-        d_gate = None
-    else:
+    if gate is not None and want_d_gate:
         d_gate = _buffer("d_gate", d_gate, gate, gate.shape, gate.dtype, index)
+    elif d_gate is not None:
+        raise ValueError("d_gate: there is none without a gate, or with want_d_gate=False")
     d_post = torch.empty_like(weight_post) if want_d_weights and weight_post is not None else None
     d_pre = torch.empty_like(weight_pre) if want_d_weights and weight_pre is not None else None
     sums = d_post is not None or d_pre is not None or (d_gate is not None and layout == 1)
