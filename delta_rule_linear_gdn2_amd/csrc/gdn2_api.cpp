@@ -528,14 +528,18 @@ gdn2_status mixer_epilogue_bwd(const void* o, const void* gate, const float* wei
     return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
 }
 
+constexpr int32_t kMaxHeads = 1 << 20;  // a token's channels and filter taps stay far inside 32 bits
+
+// Byte counts of [rows, T, H, d] tensors stay far inside 64 bits.
+bool tokens_ok(int64_t rows, int64_t T, int64_t H) { return H <= kMaxHeads && rows * T <= kMaxRows / H; }
+
 size_t prologue_bwd_workspace(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t K)
 {
     if (B <= 0 || T <= 0 || H <= 0 || !supported_head(dk) || !supported_head(dv) || K < 1 || K > 16) return 0;
+    if (!tokens_ok(B, T, H)) return 0;
     const int64_t run = gdn2::prologue_bwd_run(B, T, H, dk, dv, K), runs = (int64_t(T) + run - 1) / run;
     return align256(size_t(B) * size_t(runs) * size_t(H) * size_t(2 * dk + dv) * size_t(K) * 4);
 }
-
-constexpr int32_t kMaxHeads = 1 << 20;  // a token's channels and filter taps stay far inside 32 bits
 
 gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&conv)[3], const void* const (&logit)[2],
                                const float* conv_state_in, const void* const (&d_out)[3],
@@ -550,8 +554,8 @@ gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&c
     if (cu_seqlens && (B != 1 || num_seqs <= 0)) return GDN2_ERR_BAD_SHAPE;
     if (!(eps_l2 >= 0.f)) return GDN2_ERR_BAD_SHAPE;
     if (!supported_head(dk) || !supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
-    if (H > kMaxHeads) return GDN2_ERR_BAD_SHAPE;
     const int32_t N = cu_seqlens ? num_seqs : B;
+    if (!tokens_ok(B, T, H) || !tokens_ok(N, 1, H)) return GDN2_ERR_BAD_SHAPE;
     if (T > 0)
         for (const void* p : {x[0], x[1], x[2], static_cast<const void*>(conv[0]), static_cast<const void*>(conv[1]),
                               static_cast<const void*>(conv[2]), logit[0], logit[1], d_out[0], d_out[1], d_out[2],

@@ -503,7 +503,7 @@ size_t gdn2_mixer_epilogue_bwd_workspace_bytes(int64_t rows, int32_t dv);
  * <d_b, b> + <d_w, w> + <d_conv_state_out, conv_state_out>.
  *
  *   xq .. w_logit, conv_state_in, cu_seqlens and the scalars: the forward call's
- *              (H at most 2^20).
+ *              (H at most 2^20, B T H and num_seqs H at most 2^40).
  *   d_q, d_k, d_b : [B, T, H, dk] dtype      d_v, d_w : [B, T, H, dv] dtype
  *   d_conv_state_out : [N, H * (2 dk + dv), K - 1] FP32, or NULL for zero.
  *   d_xq, d_xk, d_b_logit : [B, T, H, dk] dtype   d_xv, d_w_logit : [B, T, H, dv]

@@ -1,8 +1,8 @@
 """Limits that the training operators' C ABI checks, on a machine without a GPU."""
 import pytest
 
-from test_abi_cpu import SHAPE, lib  # noqa: F401
-from test_training_cpu import BWD, EPI, FWD, call
+from test_abi_cpu import SHAPE, fake, lib  # noqa: F401
+from test_training_cpu import BWD, EPI, FWD, PRO, call
 
 
 @pytest.mark.parametrize("eps", [2.0 ** -127, 1e-40, 1e-45, -1.0])
@@ -10,3 +10,15 @@ def test_rejects_an_eps_below_the_normal_numbers(lib, eps):  # noqa: F811
     """The reciprocal square root of a subnormal number is infinity on the device: a row of zeros would be NaN."""
     for f, args in ((lib.gdn2_block_norm_fwd, FWD), (lib.gdn2_block_norm_bwd, BWD), (lib.gdn2_mixer_epilogue_bwd, EPI)):
         assert call(f, list(args), args, dict(eps=eps)) == SHAPE
+
+
+def test_rejects_prologues_past_64_bits(lib):  # noqa: F811
+    """Sizes whose products overflow: refused, and a workspace of none."""
+    big = (1 << 31) - 1
+    for B, T, H in ((big, big, 1 << 20), (big, big, 1), (1 << 20, 1 << 20, 2), (1 << 20, big, 1 << 20)):
+        assert call(lib.gdn2_mixer_prologue_bwd, list(PRO), PRO, dict(B=B, T=T, H=H, ws=None, ws_bytes=0)) == SHAPE
+        assert lib.gdn2_mixer_prologue_bwd_workspace_bytes(B, T, H, 64, 64, 4) == 0
+    packed = dict(B=1, cu=fake(40), num_seqs=big, H=1 << 20)
+    assert call(lib.gdn2_mixer_prologue_bwd, list(PRO), PRO, packed) == SHAPE
+    n = lib.gdn2_mixer_prologue_bwd_workspace_bytes(1 << 10, 1 << 20, 1 << 10, 64, 64, 4)  # the most tokens times heads
+    assert n > 1 << 40
