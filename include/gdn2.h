@@ -467,7 +467,7 @@ gdn2_status gdn2_block_norm_bwd(const void* x_out, const void* u, const void* ga
                                 gdn2_dtype dtype, gdn2_dtype residual_dtype, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
-/* Workspace of gdn2_block_norm_bwd: up to 768 partial rows of 3 x D FP32 sums,
+/* Workspace of gdn2_block_norm_bwd: up to 1024 partial rows of 3 x D FP32 sums,
  * rounded up to 256 bytes.  0 for invalid sizes and for rows = 0. */
 size_t gdn2_block_norm_bwd_workspace_bytes(int64_t rows, int32_t D);
 

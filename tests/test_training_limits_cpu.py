@@ -12,6 +12,17 @@ def test_rejects_an_eps_below_the_normal_numbers(lib, eps):  # noqa: F811
         assert call(f, list(args), args, dict(eps=eps)) == SHAPE
 
 
+@pytest.mark.parametrize("rows", [1, 1000, 1 << 20, 1 << 30])
+def test_block_workspace_stays_under_its_documented_bound(lib, rows):  # noqa: F811
+    """At most 1024 partial rows of 3 x D sums at every width (rounded up to 256 bytes), as the header says."""
+    most = 0
+    for D in range(1, 16385):
+        n = lib.gdn2_block_norm_bwd_workspace_bytes(rows, D)
+        assert 0 < n <= (1024 * 3 * D * 4 + 255) // 256 * 256, D
+        most = max(most, n / (3 * D * 4))
+    assert most >= min(1000, rows)  # the bound is no larger than it has to be
+
+
 def test_rejects_prologues_past_64_bits(lib):  # noqa: F811
     """Sizes whose products overflow: refused, and a workspace of none."""
     big = (1 << 31) - 1
