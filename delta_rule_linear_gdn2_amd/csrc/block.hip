@@ -31,9 +31,14 @@ namespace gdn2 {
 namespace {
 
 // Wavefronts per SIMD that the register budget is set for; a launch is as many
-// workgroups as are resident with it, so that each walks the same number of
-// rows (32768 x 2048 bf16 with an FP32 stream: 190 us with 2048 workgroups, 178 with
-// 1024, and 183, 185 and 186 with five, six and seven a SIMD).
+// workgroups as are resident with it, so that each walks the same number of rows.
+// Four where a lane holds eight channels (32768 x 2048 bf16 with an FP32 stream, in
+// four such wavefronts a row: 190 us with 2048 workgroups, 178 with the 1024 that are
+// resident, and 183, 185 and 186 at five, six and seven a SIMD).  Two wavefronts of
+// sixteen a row, the cover of those rows now, take registers for two a SIMD: 512
+// workgroups, 176 us.  Sixteen wavefronts are a workgroup of four a SIMD anyway, and
+// above 8192 channels their 128 registers spill (36 to 252 bytes a lane, in all but
+// whole bf16 rows with a bf16 stream).  FP32 ragged rows of 2049 to 4096 spill 52.
 constexpr int fwd_waves_per_simd(int WPR, int NI)
 {
     return NI == 1 || WPR == 16 ? 4 : WPR == 4 ? 3 : 2;

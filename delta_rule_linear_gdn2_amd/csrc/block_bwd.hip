@@ -1,10 +1,10 @@
 // Gradients of the step from one block of a layer to the next (formulas:
 // block.hip), for gfx950.
 //
-// 16 bytes of HBM an element (bf16, full gate) and about 56 vector instructions
-// (13 of them the dropout's bits, 12 the gate): at 32768 x 2048 HBM bounds it (206 us
+// 16 bytes of HBM an element (bf16, full gate) and about 61 vector instructions
+// (15 of them the dropout, 12 the gate): at 32768 x 2048 HBM bounds it (208 to 214 us
 // a call, 1.08 GB, the rate of a large copy), in rows that leave lanes idle the
-// instructions do (24424 rows of 1371: 131 us, 81% of that rate).  So a row is read
+// instructions do (24424 rows of 1371: 129 us, 82% of that rate).  So a row is read
 // once and held in registers: the stream's side (x', dh, dx') makes t, and its
 // registers take the next row's loads while the block's side (u, gate) is worked
 // on, and the other way round, so the next row is always on its way without a
@@ -22,7 +22,9 @@ namespace {
 
 // Wavefronts per SIMD that the register budget is set for: three (168 registers)
 // where a lane holds eight channels, two (256) at sixteen; sixteen wavefronts
-// are a workgroup of four a SIMD anyway.
+// are a workgroup of four a SIMD anyway, and above 8192 channels their 128 registers
+// spill 344 to 488 bytes a lane.  Rows under eight elements spill up to 156 without a
+// channel gate.
 constexpr int bwd_waves_per_simd(int WPR, int NI) { return NI == 1 ? 3 : WPR == 16 ? 4 : 2; }
 
 // The backward pass's covers: three wavefronts for rows of 1025 to 1536 channels,

@@ -234,7 +234,7 @@ struct Channels<float, CPL> {
 
 // Filters, window, unfinished and filter gradients take (4 KM + 8) registers a
 // channel: with eight channels a lane, four taps spilled (640 us at the shape above,
-// one wavefront a SIMD); four a lane fit 177 registers.
+// one wavefront a SIMD); four a lane fit 185 (FP32 202).
 constexpr int channels_per_lane(int KM) { return KM <= 1 ? 8 : KM <= 4 ? 4 : 2; }
 constexpr int kStep = 4;  // tokens per unrolled step
 

@@ -422,7 +422,8 @@ typedef enum gdn2_block_gate {
  *   h        : [rows, D] dtype; NULL exactly when weight_pre is NULL.
  *   residual_dtype is dtype, or FP32 with bf16 blocks (FP32 blocks with a bf16
  *   stream: GDN2_ERR_BAD_DTYPE).  1 <= D <= 16384 (above: GDN2_ERR_UNSUPPORTED),
- *   any D, at full speed for multiples of 8.  rows >= 0.  eps >= 2^-126 (a normal
+ *   any D, fastest at multiples of 8 that fill a power of two of lanes (up to
+ *   8192; wider rows spill registers).  rows >= 0.  eps >= 2^-126 (a normal
  *   FP32 number: a row of zeros takes 1 / sqrt(eps); below: GDN2_ERR_BAD_SHAPE).
  * Outputs must not overlap inputs (but x_out = x) or each other.  The norms'
  * sums of D squares are FP32: a row whose sum passes 3e38 (entries of 1e19, or
