@@ -1,6 +1,7 @@
 """Limits that the training operators' C ABI checks, on a machine without a GPU."""
 import pytest
 
+import test_training_cpu
 from test_abi_cpu import SHAPE, fake, lib  # noqa: F401
 from test_training_cpu import BWD, EPI, FWD, PRO, call
 
@@ -33,3 +34,9 @@ def test_rejects_prologues_past_64_bits(lib):  # noqa: F811
     assert call(lib.gdn2_mixer_prologue_bwd, list(PRO), PRO, packed) == SHAPE
     n = lib.gdn2_mixer_prologue_bwd_workspace_bytes(1 << 10, 1 << 20, 1 << 10, 64, 64, 4)  # the most tokens times heads
     assert n > 1 << 40
+
+
+@pytest.mark.parametrize("kw,expected", test_training_cpu.test_mixer_prologue_bwd_rejects.pytestmark[0].args[1])
+def test_mixer_prologue_bwd_zeroed_rejects(lib, kw, expected):  # noqa: F811
+    """The checks of gdn2_mixer_prologue_bwd."""
+    assert call(lib.gdn2_mixer_prologue_bwd_zeroed, list(PRO), PRO, kw) == expected
