@@ -13,6 +13,11 @@ Two entry points, both hand-written HIP behind the C ABI in include/gdn2.h:
 * ``gdn2_block_norm_fwd`` / ``gdn2_block_norm_bwd``: the step from one block of a layer
   to the next (norms, gate, residual scale, dropout) and its gradients
 * ``gdn2_dropout``        counter-based dropout whose mask is never stored
+* ``gdn2_linear_attn_fwd`` / ``gdn2_linear_attn_bwd`` / ``gdn2_linear_attn_step``: linear
+  attention with a fixed decay for each head (no erase gate) over whole sequences,
+  its gradients, and its decode step
+* ``gdn2_qk_norm_rope`` / ``gdn2_qk_norm_rope_bwd``: norms of queries and keys for each
+  head with the position rotation, and their gradients
 * ``gdn2_chunk_fwd_gates`` / ``gdn2_recurrent_step_gates``: the same with a gate
   layout (``GATES_*`` flags: scalar erase, write or decay gates, tied write gate)
 
@@ -36,12 +41,20 @@ from .binding import (  # noqa: F401
     gdn2_chunk_fwd_gates,
     gdn2_chunk_fwd_workspace_bytes,
     gdn2_dropout,
+    gdn2_linear_attn_bwd,
+    gdn2_linear_attn_bwd_workspace_bytes,
+    gdn2_linear_attn_fwd,
+    gdn2_linear_attn_fwd_workspace_bytes,
+    gdn2_linear_attn_step,
     gdn2_mixer_epilogue,
     gdn2_mixer_epilogue_bwd,
     gdn2_mixer_epilogue_bwd_workspace_bytes,
     gdn2_mixer_prologue,
     gdn2_mixer_prologue_bwd,
     gdn2_mixer_prologue_bwd_workspace_bytes,
+    gdn2_qk_norm_rope,
+    gdn2_qk_norm_rope_bwd,
+    gdn2_qk_norm_rope_bwd_workspace_bytes,
     gdn2_recurrent_fwd,
     gdn2_recurrent_step,
     gdn2_recurrent_step_gates,
@@ -67,12 +80,20 @@ __all__ = [
     "gdn2_chunk_fwd_gates",
     "gdn2_chunk_fwd_workspace_bytes",
     "gdn2_dropout",
+    "gdn2_linear_attn_bwd",
+    "gdn2_linear_attn_bwd_workspace_bytes",
+    "gdn2_linear_attn_fwd",
+    "gdn2_linear_attn_fwd_workspace_bytes",
+    "gdn2_linear_attn_step",
     "gdn2_mixer_epilogue",
     "gdn2_mixer_epilogue_bwd",
     "gdn2_mixer_epilogue_bwd_workspace_bytes",
     "gdn2_mixer_prologue",
     "gdn2_mixer_prologue_bwd",
     "gdn2_mixer_prologue_bwd_workspace_bytes",
+    "gdn2_qk_norm_rope",
+    "gdn2_qk_norm_rope_bwd",
+    "gdn2_qk_norm_rope_bwd_workspace_bytes",
     "gdn2_recurrent_fwd",
     "gdn2_recurrent_step",
     "gdn2_recurrent_step_gates",

@@ -30,9 +30,12 @@ EXPORTS = ("gdn2_block_norm_bwd", "gdn2_block_norm_bwd_workspace_bytes", "gdn2_b
            "gdn2_chunk_bwd", "gdn2_chunk_bwd_noalloc", "gdn2_chunk_bwd_noalloc_max_workspace_bytes",
            "gdn2_chunk_bwd_workspace_bytes", "gdn2_chunk_fwd", "gdn2_chunk_fwd_gates",
            "gdn2_chunk_fwd_workspace_bytes", "gdn2_dropout",
+           "gdn2_linear_attn_bwd", "gdn2_linear_attn_bwd_workspace_bytes", "gdn2_linear_attn_fwd",
+           "gdn2_linear_attn_fwd_workspace_bytes", "gdn2_linear_attn_step",
            "gdn2_mixer_epilogue", "gdn2_mixer_epilogue_bwd", "gdn2_mixer_epilogue_bwd_workspace_bytes",
            "gdn2_mixer_prologue", "gdn2_mixer_prologue_bwd", "gdn2_mixer_prologue_bwd_workspace_bytes",
            "gdn2_mixer_prologue_bwd_zeroed",
+           "gdn2_qk_norm_rope", "gdn2_qk_norm_rope_bwd", "gdn2_qk_norm_rope_bwd_workspace_bytes",
            "gdn2_recurrent_fwd", "gdn2_recurrent_step",
            "gdn2_recurrent_step_gates", "gdn2_status_string", "gdn2_version")
 
@@ -120,6 +123,21 @@ def load(path: str = LIB_PATH):
         f.restype = ctypes.c_int
     lib.gdn2_mixer_prologue_bwd_workspace_bytes.argtypes = [I] * 6
     lib.gdn2_mixer_prologue_bwd_workspace_bytes.restype = Z
+    lib.gdn2_linear_attn_fwd.argtypes = [P] * 8 + [I] * 8 + [P, Z, P]
+    lib.gdn2_linear_attn_fwd.restype = ctypes.c_int
+    lib.gdn2_linear_attn_bwd.argtypes = [P] * 12 + [I] * 8 + [P, Z, P]
+    lib.gdn2_linear_attn_bwd.restype = ctypes.c_int
+    for f in (lib.gdn2_linear_attn_fwd_workspace_bytes, lib.gdn2_linear_attn_bwd_workspace_bytes):
+        f.argtypes = [I] * 7
+        f.restype = Z
+    lib.gdn2_linear_attn_step.argtypes = [P] * 6 + [I] * 5 + [P]
+    lib.gdn2_linear_attn_step.restype = ctypes.c_int
+    lib.gdn2_qk_norm_rope.argtypes = [P] * 8 + [I] * 7 + [F, F, I, P]
+    lib.gdn2_qk_norm_rope.restype = ctypes.c_int
+    lib.gdn2_qk_norm_rope_bwd.argtypes = [P] * 12 + [I] * 7 + [F, F, I, P, Z, P]
+    lib.gdn2_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.gdn2_qk_norm_rope_bwd_workspace_bytes.argtypes = [I] * 5
+    lib.gdn2_qk_norm_rope_bwd_workspace_bytes.restype = Z
     lib.gdn2_status_string.argtypes = [ctypes.c_int]
     lib.gdn2_status_string.restype = ctypes.c_char_p
     lib.gdn2_version.argtypes = []
@@ -856,3 +874,196 @@ def gdn2_mixer_prologue_bwd(xq, xk, xv, conv_q, conv_k, conv_v, b_logit, w_logit
          *[_addr(t) for t in out.values()], _addr(cu_seqlens), B, T, H, dk, dv, K, N, q_scale, eps_l2, code,
          _addr(workspace), ws_bytes)
     return out
+
+
+# --- linear attention with a fixed decay for each head -----------------------
+
+
+def _four(name, t):
+    if len(t.shape) != 4:
+        raise ValueError(f"{name}: [B, T, H, d] (got {tuple(t.shape)})")
+    return t.shape
+
+
+@functools.lru_cache(maxsize=256)
+def gdn2_linear_attn_fwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code) -> int:
+    return int(load().gdn2_linear_attn_fwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code))
+
+
+@functools.lru_cache(maxsize=256)
+def gdn2_linear_attn_bwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code) -> int:
+    return int(load().gdn2_linear_attn_bwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code))
+
+
+@_on_stream
+def gdn2_linear_attn_fwd(q, k, v, alpha, initial_state=None, *, output_final_state=True, final_state=None, out=None,
+                         cu_seqlens=None, segmented=True, workspace=None):
+    """Linear attention with a fixed decay for each head over whole sequences:
+    S_t = alpha S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.  Returns ``(o, final_state)``
+    (final_state None if not wanted).
+
+    q, k: [B, T, H, dk]; v: [B, T, H, dv] (float32 or bfloat16, all the same);
+    alpha: [H] float32, a constant of the layer; initial_state: [N, H, dk, dv]
+    float32 or None; cu_seqlens: int32 [N + 1] on the device or None (then B must
+    be 1).  ``final_state`` may be passed (the initial_state tensor itself for an
+    in-place update).  Tokens that no packed sequence owns are not read: their
+    rows are zero in a new output, and stay as they were in a given ``out``.
+    ``segmented=False`` walks each sequence in one piece (no workspace);
+    ``workspace`` (uint8) is allocated when not given.
+    """
+    B, T, H, dk = _four("q", q)
+    dv, dt, index = _four("v", v)[3], q.dtype, q.get_device()
+    code = _code(dt)
+    N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    _expect("q", q, q.shape, dt, index)
+    _expect("k", k, q.shape, dt, index)
+    _expect("v", v, (B, T, H, dv), dt, index)
+    _expect("alpha", alpha, (H,), torch.float32, index)
+    st_shape = (N, H, dk, dv)
+    if initial_state is not None:
+        _expect("initial_state", initial_state, st_shape, torch.float32, index)
+    if cu_seqlens is not None:
+        _expect("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index)
+    new = out is None
+    out = _buffer("out", out, v, v.shape, dt, index)
+    if final_state is not None:
+        _expect("final_state", final_state, st_shape, torch.float32, index)
+    elif output_final_state:
+        final_state = alpha.new_empty(st_shape)
+    packed = N if cu_seqlens is not None else 0
+    need = gdn2_linear_attn_fwd_workspace_bytes(B, T, H, dk, dv, packed, code) if segmented else 0
+    workspace, ws_bytes = _workspace(workspace, need, q)
+    _run("gdn2_linear_attn_fwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), _addr(initial_state),
+         _addr(final_state), out.data_ptr(), _addr(cu_seqlens), B, T, H, dk, dv, packed, new, code, _addr(workspace),
+         ws_bytes)
+    return out, final_state
+
+
+@_on_stream
+def gdn2_linear_attn_bwd(q, k, v, alpha, d_o, *, initial_state=None, d_final_state=None, output_d_initial_state=False,
+                         cu_seqlens=None, segmented=True, workspace=None):
+    """Gradients of gdn2_linear_attn_fwd for the loss <d_o, o> + <d_final_state,
+    final_state>: dict(dq, dk, dv, d_initial_state), the last None when not
+    wanted.  The inputs are the forward call's; d_o: like its o; d_final_state:
+    [N, H, dk, dv] float32 or None for zero.  alpha has no gradient.  Gradients
+    of tokens that no packed sequence owns are zero.  ``segmented`` and
+    ``workspace`` as in the forward call.
+    """
+    B, T, H, dk = _four("q", q)
+    dv, dt, index = _four("v", v)[3], q.dtype, q.get_device()
+    code = _code(dt)
+    N = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    _expect("q", q, q.shape, dt, index)
+    _expect("k", k, q.shape, dt, index)
+    _expect("v", v, (B, T, H, dv), dt, index)
+    _expect("d_o", d_o, v.shape, dt, index)
+    _expect("alpha", alpha, (H,), torch.float32, index)
+    st_shape = (N, H, dk, dv)
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        if t is not None:
+            _expect(name, t, st_shape, torch.float32, index)
+    if cu_seqlens is not None:
+        _expect("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, index)
+    new = torch.empty_like
+    out = {"dq": new(q), "dk": new(k), "dv": new(v),
+           "d_initial_state": alpha.new_empty(st_shape) if output_d_initial_state else None}
+    packed = N if cu_seqlens is not None else 0
+    need = gdn2_linear_attn_bwd_workspace_bytes(B, T, H, dk, dv, packed, code) if segmented else 0
+    workspace, ws_bytes = _workspace(workspace, need, q)
+    _run("gdn2_linear_attn_bwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), _addr(initial_state),
+         d_o.data_ptr(), _addr(d_final_state), *[_addr(t) for t in out.values()], _addr(cu_seqlens), B, T, H, dk, dv,
+         packed, True, code, _addr(workspace), ws_bytes)
+    return out
+
+
+@_on_stream
+def gdn2_linear_attn_step(q, k, v, alpha, state, *, out=None):
+    """One decode step of the same layer; updates ``state`` in place, returns o.
+
+    q, k: [N, H, dk]; v: [N, H, dv]; alpha: [H] float32; state: [N, H, dk, dv]
+    float32."""
+    if len(q.shape) != 3 or len(v.shape) != 3:
+        raise ValueError(f"q, v: [N, H, d] (got {tuple(q.shape)}, {tuple(v.shape)})")
+    (N, H, dk), dv, dt, index = q.shape, v.shape[2], q.dtype, q.get_device()
+    _expect("q", q, q.shape, dt, index)
+    _expect("k", k, q.shape, dt, index)
+    _expect("v", v, (N, H, dv), dt, index)
+    _expect("alpha", alpha, (H,), torch.float32, index)
+    _expect("state", state, (N, H, dk, dv), torch.float32, index)
+    out = _buffer("out", out, v, v.shape, dt, index)
+    _run("gdn2_linear_attn_step", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), state.data_ptr(),
+         out.data_ptr(), N, H, dk, dv, _code(dt))
+    return out
+
+
+def _qk_inputs(q, k, inv_freq, positions, weight_q, weight_k):
+    """Checks what the two directions of the q, k norm and rotation share;
+    returns its sizes, type and device index."""
+    (B, T, Hq, d), dt, index = _four("q", q), q.dtype, q.get_device()
+    Hk = _four("k", k)[2]
+    _expect("q", q, q.shape, dt, index)
+    _expect("k", k, (B, T, Hk, d), dt, index)
+    if weight_q is not None:
+        _expect("weight_q", weight_q, (d,), torch.float32, index)
+    if weight_k is not None:
+        _expect("weight_k", weight_k, (d,), torch.float32, index)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _expect("inv_freq", inv_freq, (rot // 2,), torch.float32, index)
+        if not rot:
+            inv_freq = None
+    if positions is not None:
+        _expect("positions", positions, (B, T), torch.int32, index)
+    return B, T, Hq, Hk, d, rot, _code(dt), index, _addr(inv_freq)
+
+
+@_on_stream
+def gdn2_qk_norm_rope(q, k, inv_freq=None, *, positions=None, weight_q=None, weight_k=None, q_scale=1.0, eps=1e-6,
+                      interleaved=False, q_out=None, k_out=None):
+    """Queries and keys normalised for each head and rotated by their position:
+    returns ``(q_out, k_out)``.
+
+        n = x / sqrt(mean(x^2) + eps) * weight         (over a head's d channels)
+        y = scale * rotate(n, position)                (scale: q_scale for q, 1 for k)
+
+    q: [B, T, Hq, d], k: [B, T, Hk, d] (float32 or bfloat16); weight_q, weight_k:
+    [d] float32 or None (ones); inv_freq: [rot / 2] float32, the rotation's
+    frequency for each pair, or None (no rotation); positions: [B, T] int32 or
+    None (the token's index in its row).  Pairs are channels (i, i + rot / 2), or
+    (2 i, 2 i + 1) with ``interleaved``; channels from rot on are not turned.
+    q_out may be q and k_out may be k (in place); they are allocated when not
+    given.
+    """
+    B, T, Hq, Hk, d, rot, code, index, freq = _qk_inputs(q, k, inv_freq, positions, weight_q, weight_k)
+    q_out = _buffer("q_out", q_out, q, q.shape, q.dtype, index)
+    k_out = _buffer("k_out", k_out, k, k.shape, k.dtype, index)
+    _run("gdn2_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), _addr(weight_q), _addr(weight_k), freq, _addr(positions),
+         q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hk, d, rot, interleaved, q_scale, eps, code)
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=256)
+def gdn2_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, d) -> int:
+    return int(load().gdn2_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, d))
+
+
+@_on_stream
+def gdn2_qk_norm_rope_bwd(q, k, d_q_out, d_k_out, inv_freq=None, *, positions=None, weight_q=None, weight_k=None,
+                          q_scale=1.0, eps=1e-6, interleaved=False, want_d_weights=True, workspace=None):
+    """Gradients of gdn2_qk_norm_rope for the loss <d_q_out, q_out> + <d_k_out,
+    k_out>: dict(d_q, d_k, d_weight_q, d_weight_k), None in the place of what has
+    no weight or is not wanted.  q and k are the forward call's inputs (not its
+    outputs).  ``workspace`` (uint8) is allocated when not given."""
+    B, T, Hq, Hk, d, rot, code, index, freq = _qk_inputs(q, k, inv_freq, positions, weight_q, weight_k)
+    _expect("d_q_out", d_q_out, q.shape, q.dtype, index)
+    _expect("d_k_out", d_k_out, k.shape, k.dtype, index)
+    d_q, d_k = torch.empty_like(q), torch.empty_like(k)
+    dw_q = torch.empty_like(weight_q) if want_d_weights and weight_q is not None else None
+    dw_k = torch.empty_like(weight_k) if want_d_weights and weight_k is not None else None
+    need = gdn2_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, d) if dw_q is not None or dw_k is not None else 0
+    workspace, ws_bytes = _workspace(workspace, need, q)
+    _run("gdn2_qk_norm_rope_bwd", index, q.data_ptr(), k.data_ptr(), _addr(weight_q), _addr(weight_k), freq,
+         _addr(positions), d_q_out.data_ptr(), d_k_out.data_ptr(), d_q.data_ptr(), d_k.data_ptr(), _addr(dw_q),
+         _addr(dw_k), B, T, Hq, Hk, d, rot, interleaved, q_scale, eps, code, _addr(workspace), ws_bytes)
+    return {"d_q": d_q, "d_k": d_k, "d_weight_q": dw_q, "d_weight_k": dw_k}

@@ -29,6 +29,9 @@ SOURCES = [
     "mixer_bwd.hip",
     "block.hip",
     "block_bwd.hip",
+    "linear_attn.hip",
+    "linear_step.hip",
+    "qk_rope.hip",
     "colsum.hip",
     "scratch.hip",
     "segments.hip",

@@ -355,6 +355,8 @@ gdn2_status check_spans(std::initializer_list<Span> in, std::initializer_list<Sp
     return GDN2_OK;
 }
 
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
 bool misaligned(std::initializer_list<const void*> ptrs)
 {
     for (const void* p : ptrs)
@@ -607,6 +609,286 @@ gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&c
     a.run = gdn2::prologue_bwd_run(B, T, H, dk, dv, K);
     a.partial = need ? static_cast<float*>(workspace) : nullptr;
     const hipError_t e = gdn2::launch_mixer_prologue_bwd(a, dtype == GDN2_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+// ---- linear attention with a fixed decay for each head ----------------------
+
+constexpr int32_t kLinearMaxHeads = 1 << 15;  // a chunk's rows stay inside the 32 bits of a buffer offset
+
+// Segments of the walks over sequences, and what their carries take.  A walk is
+// one workgroup per (segment, head, column slice, walk); `subs` of them share a
+// segment and head.
+//   batch:  as many segments a row as fill the compute units once, none shorter
+//           than four chunks
+//   packed: the lengths are on the device.  Segments of the share that each
+//           compute unit has of the whole, so that one long sequence does not
+//           outlast all others.
+struct LinearPlan {
+    int32_t seg_len = 0, segments = 1;
+    int64_t slots = 0;
+    size_t carry_bytes = 0;  // one state per slot and head
+};
+
+int32_t linear_slices(int32_t width) { return width % 64 == 0 ? width / 64 : 1; }
+
+LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, int32_t subs, int32_t cus)
+{
+    constexpr int64_t kShortest = 4 * gdn2::kLinearChunk;
+    LinearPlan p;
+    const int64_t rows = num_seqs > 0 ? num_seqs : B;
+    p.seg_len = T > 0 ? T : 1;
+    p.slots = rows;
+    const int64_t groups = int64_t(num_seqs > 0 ? 1 : B) * H * subs;  // workgroups that walk T tokens
+    int64_t len;
+    if (num_seqs > 0) {
+        len = int64_t(T) * groups / cus;
+    } else {
+        const int64_t fit = cus / groups;
+        if (fit < 2) return p;
+        len = (T + fit - 1) / fit;
+    }
+    len = std::max((len + gdn2::kLinearChunk - 1) / gdn2::kLinearChunk * gdn2::kLinearChunk, kShortest);
+    if (len >= T) return p;
+    p.seg_len = int32_t(len);
+    p.segments = int32_t((T + len - 1) / len);
+    p.slots = num_seqs > 0 ? T / len + num_seqs : rows * p.segments;
+    p.carry_bytes = align256(size_t(p.slots) * size_t(H) * size_t(dk) * size_t(dv) * 4);
+    return p;
+}
+
+bool linear_sizes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs)
+{
+    return B > 0 && T >= 0 && H > 0 && H <= kLinearMaxHeads && num_seqs >= 0 && tokens_ok(B, T, H) &&
+           tokens_ok(num_seqs, 1, H) && tokens_ok(B, 1, H) && supported_head(dk) && supported_head(dv);
+}
+
+LinearPlan linear_fwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs)
+{
+    return linear_plan(B, T, H, dk, dv, num_seqs, linear_slices(dv), device_cus());
+}
+
+LinearPlan linear_bwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs)
+{
+    return linear_plan(B, T, H, dk, dv, num_seqs, 2 * linear_slices(dk) + linear_slices(dv), device_cus());
+}
+
+gdn2::LinearLaunch linear_launch(const float* alpha, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t N,
+                                 const LinearPlan& p, bool zero_padding)
+{
+    gdn2::LinearLaunch a{};
+    a.alpha = alpha;
+    a.cu_seqlens = cu_seqlens;
+    a.B = B, a.T = T, a.H = H, a.N = N;
+    a.seg_len = p.seg_len, a.segments = p.segments;
+    a.units = p.slots * H;
+    a.pad_blocks = cu_seqlens && zero_padding && T > 0 ? 64 : 0;
+    return a;
+}
+
+// The sizes, pointers and type that both directions check alike.
+gdn2_status linear_check(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, const float* alpha,
+                         const int32_t* cu_seqlens, gdn2_dtype dtype)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    if (B <= 0 || T < 0 || H <= 0 || dk <= 0 || dv <= 0) return GDN2_ERR_BAD_SHAPE;
+    if (cu_seqlens && (B != 1 || num_seqs <= 0)) return GDN2_ERR_BAD_SHAPE;
+    if (!supported_head(dk) || !supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
+    if (!linear_sizes(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0)) return GDN2_ERR_BAD_SHAPE;
+    if (!alpha) return GDN2_ERR_NULL_POINTER;
+    if (misaligned4(alpha) || misaligned4(cu_seqlens)) return GDN2_ERR_MISALIGNED;
+    return GDN2_OK;
+}
+
+gdn2_status linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha, const float* initial_state,
+                            float* final_state, void* o, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H,
+                            int32_t dk, int32_t dv, int32_t num_seqs, bool zero_padding, gdn2_dtype dtype,
+                            void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (gdn2_status s = linear_check(B, T, H, dk, dv, num_seqs, alpha, cu_seqlens, dtype)) return s;
+    const int32_t N = cu_seqlens ? num_seqs : B;
+    if (T > 0 && (!q || !k || !v || !o)) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({q, k, v, o, initial_state, final_state, workspace})) return GDN2_ERR_MISALIGNED;
+    LinearPlan p = linear_fwd_plan(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0);
+    if (!workspace && p.carry_bytes) {  // one segment a sequence
+        p = LinearPlan{};
+        p.seg_len = T;
+        p.slots = N;
+    }
+    if (workspace && workspace_bytes < p.carry_bytes) return GDN2_ERR_WORKSPACE;
+    const int64_t rows = int64_t(B) * T * H, nk = rows * dk * element_bytes(dtype), nv = rows * dv * element_bytes(dtype);
+    const int64_t st = int64_t(N) * H * dk * dv * 4;
+    if (gdn2_status s = check_spans({span_or_none(q, nk), span_or_none(k, nk), span_or_none(v, nv), span_or_none(alpha, H * 4),
+                                     span_or_none(initial_state, st), span_or_none(cu_seqlens, int64_t(N + 1) * 4)},
+                                    {span_or_none(final_state, st), span_or_none(o, nv),
+                                     span_or_none(p.carry_bytes ? workspace : nullptr, int64_t(p.carry_bytes))}, 0, 4))
+        return s;
+    const bool bf16 = dtype == GDN2_DTYPE_BF16;
+    gdn2::LinearLaunch a = linear_launch(alpha, cu_seqlens, B, T, H, N, p, zero_padding);
+    a.walks = 1;
+    a.width = dv;
+    a.walk[0] = {q, k, v, o, initial_state, final_state, static_cast<float*>(p.carry_bytes ? workspace : nullptr), dv, 1, 0};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = p.segments > 1 ? gdn2::launch_linear_walk(a, dk, true, bf16, s) : hipSuccess;
+    if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, bf16, s);
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+gdn2_status linear_attn_bwd(const void* q, const void* k, const void* v, const float* alpha, const float* initial_state,
+                            const void* d_o, const float* d_final_state, void* dq, void* dk_, void* dv_,
+                            float* d_initial_state, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t dk,
+                            int32_t dv, int32_t num_seqs, bool zero_padding, gdn2_dtype dtype, void* workspace,
+                            size_t workspace_bytes, void* stream)
+{
+    if (gdn2_status s = linear_check(B, T, H, dk, dv, num_seqs, alpha, cu_seqlens, dtype)) return s;
+    const int32_t N = cu_seqlens ? num_seqs : B;
+    if (T > 0 && (!q || !k || !v || !d_o || !dq || !dk_ || !dv_)) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({q, k, v, d_o, initial_state, d_final_state, dq, dk_, dv_, d_initial_state, workspace}))
+        return GDN2_ERR_MISALIGNED;
+    LinearPlan p = linear_bwd_plan(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0);
+    if (!workspace && p.carry_bytes) {
+        p = LinearPlan{};
+        p.seg_len = T;
+        p.slots = N;
+    }
+    const size_t need = 2 * p.carry_bytes;
+    if (workspace && workspace_bytes < need) return GDN2_ERR_WORKSPACE;
+    const int64_t rows = int64_t(B) * T * H, nk = rows * dk * element_bytes(dtype), nv = rows * dv * element_bytes(dtype);
+    const int64_t st = int64_t(N) * H * dk * dv * 4;
+    if (gdn2_status s = check_spans({span_or_none(q, nk), span_or_none(k, nk), span_or_none(v, nv), span_or_none(alpha, H * 4),
+                                     span_or_none(initial_state, st), span_or_none(d_o, nv), span_or_none(d_final_state, st),
+                                     span_or_none(cu_seqlens, int64_t(N + 1) * 4)},
+                                    {span_or_none(dq, nk), span_or_none(dk_, nk), span_or_none(dv_, nv),
+                                     span_or_none(d_initial_state, st),
+                                     span_or_none(need ? workspace : nullptr, int64_t(need))}))
+        return s;
+    const bool bf16 = dtype == GDN2_DTYPE_BF16;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    float* const carry_s = static_cast<float*>(need ? workspace : nullptr);
+    float* const carry_r = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.carry_bytes) : nullptr;
+    gdn2::LinearLaunch a = linear_launch(alpha, cu_seqlens, B, T, H, N, p, zero_padding);
+    hipError_t e = hipSuccess;
+    if (p.segments > 1) {
+        // the segments' own states, and gradients of states
+        a.walks = 2;
+        a.width = dv;
+        a.walk[0] = {nullptr, k, v, nullptr, initial_state, nullptr, carry_s, dv, 1, 0};
+        a.walk[1] = {nullptr, q, d_o, nullptr, d_final_state, nullptr, carry_r, dv, 1, 1};
+        e = gdn2::launch_linear_walk(a, dk, true, bf16, s);
+    }
+    const gdn2::LinearWalk to_k{v, d_o, q, dk_, d_final_state, nullptr, carry_r, 1, dv, 1};
+    const gdn2::LinearWalk to_v{k, q, d_o, dv_, d_final_state, d_initial_state, carry_r, dv, 1, 1};
+    const gdn2::LinearWalk to_q{d_o, v, k, dq, initial_state, nullptr, carry_s, 1, dv, 0};
+    a.walk[0] = to_k;
+    a.width = dk;
+    if (dk == dv) {  // the walks that read the same rows in the same order run side by side
+        a.walk[1] = to_v;
+        a.walk[2] = to_q;
+        a.walks = 3;
+        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, bf16, s);
+    } else {
+        a.walk[1] = to_q;
+        a.walks = 2;
+        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dv, false, bf16, s);
+        a.walk[0] = to_v;
+        a.walks = 1;
+        a.width = dv;
+        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, bf16, s);
+    }
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+gdn2_status linear_attn_step(const void* q, const void* k, const void* v, const float* alpha, float* state, void* o,
+                             int32_t N, int32_t H, int32_t dk, int32_t dv, gdn2_dtype dtype, void* stream)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    if (N < 0 || H <= 0 || dk <= 0 || dv <= 0) return GDN2_ERR_BAD_SHAPE;
+    if (!supported_head(dk) || !supported_head(dv)) return GDN2_ERR_UNSUPPORTED;
+    if (!tokens_ok(N, 1, H)) return GDN2_ERR_BAD_SHAPE;
+    if (N == 0) return GDN2_OK;
+    if (!q || !k || !v || !alpha || !state || !o) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({q, k, v, state, o}) || misaligned4(alpha)) return GDN2_ERR_MISALIGNED;
+    const int64_t rows = int64_t(N) * H, nk = rows * dk * element_bytes(dtype), nv = rows * dv * element_bytes(dtype);
+    if (gdn2_status s = check_spans({span(q, nk), span(k, nk), span(v, nv), span(alpha, int64_t(H) * 4)},
+                                    {span(state, rows * dk * dv * 4), span(o, nv)}))
+        return s;
+    const hipError_t e = gdn2::launch_linear_step({q, k, v, alpha, state, o, N, H, dk, dv}, dtype == GDN2_DTYPE_BF16,
+                                                  static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+// ---- norms of queries and keys with the position rotation --------------------
+
+bool qk_sizes(int32_t B, int32_t T, int32_t Hq, int32_t Hk)
+{
+    return B > 0 && T >= 0 && Hq > 0 && Hk > 0 && Hq <= kLinearMaxHeads && Hk <= kLinearMaxHeads && tokens_ok(B, T, Hq) &&
+           tokens_ok(B, T, Hk);
+}
+
+size_t qk_norm_rope_bwd_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t d)
+{
+    if (!qk_sizes(B, T, Hq, Hk) || !supported_head(d)) return 0;
+    return align256(size_t(gdn2::qk_rope_bwd_partials(int64_t(B) * T, Hq, Hk, d)) * 2 * size_t(d) * 4);
+}
+
+gdn2_status qk_check(int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t d, int32_t rot, const float* inv_freq,
+                     const int32_t* positions, float eps, gdn2_dtype dtype)
+{
+    if (dtype != GDN2_DTYPE_F32 && dtype != GDN2_DTYPE_BF16) return GDN2_ERR_BAD_DTYPE;
+    if (!qk_sizes(B, T, Hq, Hk) || d <= 0 || rot < 0 || rot > d || rot % 8 != 0 || !eps_ok(eps)) return GDN2_ERR_BAD_SHAPE;
+    if (!supported_head(d)) return GDN2_ERR_UNSUPPORTED;
+    if (rot > 0 && !inv_freq) return GDN2_ERR_NULL_POINTER;
+    if (rot == 0 && inv_freq) return GDN2_ERR_BAD_SHAPE;
+    if (misaligned4(positions)) return GDN2_ERR_MISALIGNED;
+    return GDN2_OK;
+}
+
+gdn2_status qk_norm_rope(const void* q, const void* k, const float* weight_q, const float* weight_k, const float* inv_freq,
+                         const int32_t* positions, void* q_out, void* k_out, int32_t B, int32_t T, int32_t Hq, int32_t Hk,
+                         int32_t d, int32_t rot, bool neighbours, float q_scale, float eps, gdn2_dtype dtype, void* stream)
+{
+    if (gdn2_status s = qk_check(B, T, Hq, Hk, d, rot, inv_freq, positions, eps, dtype)) return s;
+    if (T == 0) return GDN2_OK;
+    if (!q || !k || !q_out || !k_out) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({q, k, weight_q, weight_k, inv_freq, q_out, k_out})) return GDN2_ERR_MISALIGNED;
+    const int64_t tokens = int64_t(B) * T, row = int64_t(d) * element_bytes(dtype);
+    const Span in_q = span(q, tokens * Hq * row), in_k = span(k, tokens * Hk * row), out_q = span(q_out, tokens * Hq * row),
+               out_k = span(k_out, tokens * Hk * row);
+    const Span w[] = {span_or_none(weight_q, d * 4), span_or_none(weight_k, d * 4), span_or_none(inv_freq, rot * 2),
+                      span_or_none(positions, tokens * 4)};
+    if (gdn2_status s = check_spans({in_q, w[0], w[1], w[2], w[3]}, {out_q, out_k}, 0, 0)) return s;  // q_out may be q
+    if (gdn2_status s = check_spans({in_k}, {out_k, out_q}, 0, 0)) return s;                          // k_out may be k
+    gdn2::QkRopeArgs a{{q, k}, {q_out, k_out}, {weight_q, weight_k}, inv_freq, positions, tokens, T, {Hq, Hk}, d, rot,
+                       neighbours, q_scale, eps, 0};
+    const hipError_t e = gdn2::launch_qk_rope(a, dtype == GDN2_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
+}
+
+gdn2_status qk_norm_rope_bwd(const void* q, const void* k, const float* weight_q, const float* weight_k,
+                             const float* inv_freq, const int32_t* positions, const void* d_q_out, const void* d_k_out,
+                             void* d_q, void* d_k, float* d_weight_q, float* d_weight_k, int32_t B, int32_t T, int32_t Hq,
+                             int32_t Hk, int32_t d, int32_t rot, bool neighbours, float q_scale, float eps,
+                             gdn2_dtype dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (gdn2_status s = qk_check(B, T, Hq, Hk, d, rot, inv_freq, positions, eps, dtype)) return s;
+    if ((d_weight_q && !weight_q) || (d_weight_k && !weight_k)) return GDN2_ERR_BAD_SHAPE;
+    if (T > 0 && (!q || !k || !d_q_out || !d_k_out || !d_q || !d_k)) return GDN2_ERR_NULL_POINTER;
+    if (misaligned({q, k, weight_q, weight_k, inv_freq, d_q_out, d_k_out, d_q, d_k, d_weight_q, d_weight_k, workspace}))
+        return GDN2_ERR_MISALIGNED;
+    const size_t need = d_weight_q || d_weight_k ? qk_norm_rope_bwd_workspace(B, T, Hq, Hk, d) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN2_ERR_WORKSPACE;
+    const int64_t tokens = int64_t(B) * T, nq = tokens * Hq * d * element_bytes(dtype), nk = tokens * Hk * d * element_bytes(dtype),
+                  nw = int64_t(d) * 4;
+    if (gdn2_status s = check_spans({span_or_none(q, nq), span_or_none(k, nk), span_or_none(weight_q, nw), span_or_none(weight_k, nw),
+                                     span_or_none(inv_freq, rot * 2), span_or_none(positions, tokens * 4),
+                                     span_or_none(d_q_out, nq), span_or_none(d_k_out, nk)},
+                                    {span_or_none(d_q, nq), span_or_none(d_k, nk), span_or_none(d_weight_q, nw),
+                                     span_or_none(d_weight_k, nw), span_or_none(need ? workspace : nullptr, int64_t(need))}))
+        return s;
+    gdn2::QkRopeBwdArgs a{{q, k}, {d_q_out, d_k_out}, {d_q, d_k}, {weight_q, weight_k}, {d_weight_q, d_weight_k}, inv_freq,
+                          positions, tokens, T, {Hq, Hk}, d, rot, neighbours, q_scale, eps, 0,
+                          need ? static_cast<float*>(workspace) : nullptr};
+    const hipError_t e = gdn2::launch_qk_rope_bwd(a, dtype == GDN2_DTYPE_BF16, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
 }
 
@@ -950,6 +1232,75 @@ size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, 
                                                int32_t kernel_size)
 {
     return prologue_bwd_workspace(B, T, H, dk, dv, kernel_size);
+}
+
+gdn2_status gdn2_linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha,
+                                 const float* initial_state, float* final_state, void* o, const int32_t* cu_seqlens,
+                                 int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs,
+                                 int32_t zero_padding, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream)
+{
+    return linear_attn_fwd(q, k, v, alpha, initial_state, final_state, o, cu_seqlens, B, T, H, dk, dv, num_seqs,
+                           zero_padding != 0, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t gdn2_linear_attn_fwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs,
+                                            gdn2_dtype dtype)
+{
+    (void)dtype;
+    return linear_sizes(B, T, H, dk, dv, num_seqs) ? linear_fwd_plan(B, T, H, dk, dv, num_seqs).carry_bytes : 0;
+}
+
+gdn2_status gdn2_linear_attn_bwd(const void* q, const void* k, const void* v, const float* alpha,
+                                 const float* initial_state, const void* d_o, const float* d_final_state, void* dq,
+                                 void* dk, void* dv, float* d_initial_state, const int32_t* cu_seqlens, int32_t B,
+                                 int32_t T, int32_t H, int32_t dk_size, int32_t dv_size, int32_t num_seqs,
+                                 int32_t zero_padding, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream)
+{
+    return linear_attn_bwd(q, k, v, alpha, initial_state, d_o, d_final_state, dq, dk, dv, d_initial_state, cu_seqlens, B,
+                           T, H, dk_size, dv_size, num_seqs, zero_padding != 0, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t gdn2_linear_attn_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk_size, int32_t dv_size,
+                                            int32_t num_seqs, gdn2_dtype dtype)
+{
+    (void)dtype;
+    return linear_sizes(B, T, H, dk_size, dv_size, num_seqs)
+               ? 2 * linear_bwd_plan(B, T, H, dk_size, dv_size, num_seqs).carry_bytes
+               : 0;
+}
+
+gdn2_status gdn2_linear_attn_step(const void* q, const void* k, const void* v, const float* alpha, float* state, void* o,
+                                  int32_t N, int32_t H, int32_t dk, int32_t dv, gdn2_dtype dtype, void* stream)
+{
+    return linear_attn_step(q, k, v, alpha, state, o, N, H, dk, dv, dtype, stream);
+}
+
+gdn2_status gdn2_qk_norm_rope(const void* q, const void* k, const float* weight_q, const float* weight_k,
+                              const float* inv_freq, const int32_t* positions, void* q_out, void* k_out, int32_t B,
+                              int32_t T, int32_t Hq, int32_t Hk, int32_t d, int32_t rot, int32_t interleaved,
+                              float q_scale, float eps, gdn2_dtype dtype, void* stream)
+{
+    return qk_norm_rope(q, k, weight_q, weight_k, inv_freq, positions, q_out, k_out, B, T, Hq, Hk, d, rot,
+                        interleaved != 0, q_scale, eps, dtype, stream);
+}
+
+gdn2_status gdn2_qk_norm_rope_bwd(const void* q, const void* k, const float* weight_q, const float* weight_k,
+                                  const float* inv_freq, const int32_t* positions, const void* d_q_out,
+                                  const void* d_k_out, void* d_q, void* d_k, float* d_weight_q, float* d_weight_k,
+                                  int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t d, int32_t rot,
+                                  int32_t interleaved, float q_scale, float eps, gdn2_dtype dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream)
+{
+    return qk_norm_rope_bwd(q, k, weight_q, weight_k, inv_freq, positions, d_q_out, d_k_out, d_q, d_k, d_weight_q,
+                            d_weight_k, B, T, Hq, Hk, d, rot, interleaved != 0, q_scale, eps, dtype, workspace,
+                            workspace_bytes, stream);
+}
+
+size_t gdn2_qk_norm_rope_bwd_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t d)
+{
+    return qk_norm_rope_bwd_workspace(B, T, Hq, Hk, d);
 }
 
 }  // extern "C"

@@ -247,7 +247,82 @@ struct ColumnSumArgs {
     int64_t end[3];
 };
 
+// Linear attention with a fixed decay for each head, as walks (see
+// linear_attn.hip): x, y [B, T, H, DA], z and out [B, T, H, width].
+constexpr int kLinearChunk = 64;
+struct LinearWalk {
+    const void* x;        // null in a launch for carries only
+    const void* y;
+    const void* z;
+    void* out;
+    const float* carry_in;   // [N][H] squares, or null (zeros)
+    float* carry_out;        // [N][H] squares, or null
+    float* segment_carry;    // [slots][H] squares: a segment's own carry, or null without segments
+    int32_t state_d, state_c;  // strides of a square's row d (of DA) and column c (of width)
+    int32_t back;            // walk from the sequence's end
+};
+struct LinearLaunch {
+    LinearWalk walk[3];
+    int32_t walks;
+    const float* alpha;      // [H]
+    const int32_t* cu_seqlens;
+    int32_t B, T, H, N, width;
+    // Sequences are walked in segments of seg_len tokens: `segments` for each
+    // batch row, or, packed, slots start / seg_len + n + m (segments == 1: one
+    // slot a sequence).  units = slots x H.
+    int32_t seg_len, segments;
+    int64_t units;
+    int64_t walk_blocks;     // set by the launch
+    int32_t pad_blocks;      // blocks that write zeros to rows that no sequence owns
+};
+// Decode step: q, k [N, H, dk], v, o [N, H, dv], state [N, H, dk, dv] in place.
+struct LinearStepArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* alpha;  // [H]
+    float* state;
+    void* o;
+    int32_t N, H, dk, dv;
+};
+
+// Norms of q and k for each head, then the position rotation: x, y [tokens,
+// heads, d] for q and k.  rot channels are turned (a multiple of 8), paired by
+// halves or with their neighbours.
+struct QkRopeArgs {
+    const void* x[2];
+    void* y[2];
+    const float* weight[2];    // [d], or null (ones)
+    const float* inv_freq;     // [rot / 2]
+    const int32_t* positions;  // [tokens], or null: token % T
+    int64_t tokens;
+    int32_t T, heads[2], d, rot;
+    bool neighbours;
+    float q_scale, eps;
+    int32_t parts;             // set by the launch
+};
+struct QkRopeBwdArgs {
+    const void* x[2];
+    const void* dy[2];
+    void* dx[2];
+    const float* weight[2];
+    float* d_weight[2];        // or null
+    const float* inv_freq;
+    const int32_t* positions;
+    int64_t tokens;
+    int32_t T, heads[2], d, rot;
+    bool neighbours;
+    float q_scale, eps;
+    int32_t parts;             // set by the launch
+    float* partial;            // [qk_rope_bwd_partials(...)][2 d], or null when no d_weight is wanted
+};
+int64_t qk_rope_bwd_partials(int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t d);
+
 // Each returns hipSuccess or the launch error; bf16 selects the input dtype.
+hipError_t launch_qk_rope(QkRopeArgs a, bool bf16, hipStream_t stream);
+hipError_t launch_qk_rope_bwd(QkRopeBwdArgs a, bool bf16, hipStream_t stream);
+hipError_t launch_linear_walk(const LinearLaunch& a, int da, bool carries_only, bool bf16, hipStream_t stream);
+hipError_t launch_linear_step(const LinearStepArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream);
 hipError_t launch_dropout(const DropoutCall& a, bool bf16, hipStream_t stream);
 hipError_t launch_block_norm_fwd(const BlockNormArgs& a, bool bf16, bool residual_bf16, hipStream_t stream);

@@ -551,6 +551,137 @@ gdn2_status gdn2_mixer_prologue_bwd_zeroed(const void* xq, const void* xk, const
 size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
                                                int32_t kernel_size);
 
+/*
+ * Linear attention with a fixed decay for each head: the layer without an erase
+ * gate, whose state decays by one constant a per head (a slope of the layer, not
+ * a projection of the token; it has no gradient).  Per head, per token:
+ *     S_t = a S_{t-1} + k_t v_t^T         o_t = S_t^T q_t
+ * It is gdn2_chunk_fwd with b = 0, w = 1 and alpha = a everywhere, without the
+ * triangular solve and without gate tensors.
+ *
+ *   q, k : [B, T, H, dk] dtype      v, o : [B, T, H, dv] dtype
+ *   alpha : [H] FP32 (4-byte aligned), clamped to [2^-15, 1].
+ *   initial_state : [N, H, dk, dv] FP32, or NULL for zeros.
+ *   final_state   : [N, H, dk, dv] FP32, or NULL if not wanted.  May be
+ *                   initial_state (in place).
+ *   cu_seqlens, num_seqs : as for gdn2_chunk_fwd, but packed input may end in
+ *                   padding: tokens from cu_seqlens[num_seqs] on (and before
+ *                   cu_seqlens[0]) are not read.  Their rows of o stay as they
+ *                   were, or become zero with zero_padding != 0.
+ *   workspace     : NULL, or gdn2_linear_attn_fwd_workspace_bytes(...) bytes of
+ *                   device memory, 16-byte aligned, contents on entry irrelevant
+ *                   (smaller: GDN2_ERR_WORKSPACE).  With it, sequences are walked
+ *                   in several segments at once where there are too few of them to
+ *                   fill the device, or where packed ones may differ in length.
+ *                   Calls that may run at the same time need a workspace each.
+ * T may be 0 (then only final_state = initial_state is written).  H is at most
+ * 2^15, B T H and num_seqs H at most 2^40.  Outputs and the workspace must not
+ * overlap inputs (but final_state = initial_state) or each other.
+ *
+ * bf16 inputs feed bf16 products with FP32 sums; the states are those of FP32
+ * arithmetic, and their copy that o reads is rounded to bf16.  Inside a 64-token
+ * chunk of a sequence a NaN or infinity in v or k reaches the outputs of the
+ * chunk's earlier tokens too (they multiply it by zero).
+ */
+gdn2_status gdn2_linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha,
+                                 const float* initial_state, float* final_state, void* o, const int32_t* cu_seqlens,
+                                 int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs,
+                                 int32_t zero_padding, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Workspace of gdn2_linear_attn_fwd (num_seqs: the packed sequence count with
+ * cu_seqlens, else 0): one FP32 state per segment and head; 0 where a call runs
+ * without one, and for invalid sizes. */
+size_t gdn2_linear_attn_fwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs,
+                                            gdn2_dtype dtype);
+
+/*
+ * Gradients of gdn2_linear_attn_fwd for the loss <d_o, o> + <d_final_state,
+ * final_state>:
+ *     dq_t = S_t d_o_t                     R_t = q_t d_o_t^T + a R_{t+1}
+ *     dk_t = R_t v_t     dv_t = R_t^T k_t  d_initial_state = a R_0
+ * (the last token's R adds d_final_state).  Nothing is saved by the forward
+ * call.
+ *
+ *   q .. alpha, initial_state, cu_seqlens and the sizes: the forward call's.
+ *   d_o  : [B, T, H, dv] dtype.
+ *   d_final_state : [N, H, dk, dv] FP32, or NULL for zero.
+ *   dq, dk : [B, T, H, dk] dtype      dv : [B, T, H, dv] dtype
+ *   d_initial_state : [N, H, dk, dv] FP32, or NULL if not wanted.
+ *   zero_padding, workspace: as for the forward call, the workspace of
+ *              gdn2_linear_attn_bwd_workspace_bytes bytes.
+ * Outputs and the workspace must not overlap inputs or each other.
+ */
+gdn2_status gdn2_linear_attn_bwd(const void* q, const void* k, const void* v, const float* alpha,
+                                 const float* initial_state, const void* d_o, const float* d_final_state, void* dq,
+                                 void* dk, void* dv, float* d_initial_state, const int32_t* cu_seqlens, int32_t B,
+                                 int32_t T, int32_t H, int32_t dk_size, int32_t dv_size, int32_t num_seqs,
+                                 int32_t zero_padding, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Workspace of gdn2_linear_attn_bwd: two FP32 states per segment and head; 0 where
+ * a call runs without one, and for invalid sizes. */
+size_t gdn2_linear_attn_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk_size, int32_t dv_size,
+                                            int32_t num_seqs, gdn2_dtype dtype);
+
+/*
+ * One decode step of the same layer for N independent sequences, the states
+ * read and written once, in place.
+ *   q, k : [N, H, dk] dtype     v, o : [N, H, dv] dtype     alpha : [H] FP32
+ *   state : [N, H, dk, dv] FP32.   N may be 0; N H at most 2^40.
+ * o must not overlap any input or the state, nor the state an input.
+ */
+gdn2_status gdn2_linear_attn_step(const void* q, const void* k, const void* v, const float* alpha, float* state,
+                                  void* o, int32_t N, int32_t H, int32_t dk, int32_t dv, gdn2_dtype dtype,
+                                  void* stream);
+
+/*
+ * Queries and keys of such a layer from their projections: an RMS norm for each
+ * head, then a rotation by the token's position.  Per token and head, over its d
+ * channels:
+ *     n = x / sqrt(mean(x^2) + eps) * weight
+ *     y = scale * rotate(n, position)        (scale: q_scale for q, 1 for k)
+ * rotate turns pair i < rot / 2 by the angle position * inv_freq[i] (formed in 64
+ * bits): (c, s) its cosine and sine, the pair (n_1, n_2) becomes
+ * (n_1 c - n_2 s, n_2 c + n_1 s).  Pair i is channels (i, i + rot / 2), or with
+ * interleaved != 0 (2 i, 2 i + 1).  Channels from rot on are not turned.
+ *
+ *   q, q_out : [B, T, Hq, d] dtype      k, k_out : [B, T, Hk, d] dtype
+ *   weight_q, weight_k : [d] FP32 (shared by the heads), or NULL (ones)
+ *   inv_freq  : [rot / 2] FP32; NULL exactly when rot = 0.
+ *   positions : [B, T] int32 on the device, or NULL: the token's index in its row.
+ *   d in {32, 64, 128}; rot a multiple of 8 in [0, d]; Hq, Hk in [1, 2^15];
+ *   eps >= 2^-126.  T may be 0.
+ * q_out may be q and k_out may be k (in place); outputs must not overlap inputs
+ * or each other otherwise.  A decode step is the same call with T = 1.  The
+ * norm's sum of squares is FP32 (entries past 1e18 overflow to zeros).
+ */
+gdn2_status gdn2_qk_norm_rope(const void* q, const void* k, const float* weight_q, const float* weight_k,
+                              const float* inv_freq, const int32_t* positions, void* q_out, void* k_out, int32_t B,
+                              int32_t T, int32_t Hq, int32_t Hk, int32_t d, int32_t rot, int32_t interleaved,
+                              float q_scale, float eps, gdn2_dtype dtype, void* stream);
+
+/*
+ * Gradients of gdn2_qk_norm_rope for the loss <d_q_out, q_out> + <d_k_out, k_out>.
+ *   q, k (the forward call's inputs) and the other arguments: as in that call.
+ *   d_q_out, d_q : [B, T, Hq, d] dtype      d_k_out, d_k : [B, T, Hk, d] dtype
+ *   d_weight_q, d_weight_k : [d] FP32, or NULL if not wanted (a gradient of a weight
+ *              that is not given: GDN2_ERR_BAD_SHAPE).
+ *   workspace: gdn2_qk_norm_rope_bwd_workspace_bytes bytes, 16-byte aligned, when a
+ *              weight's gradient is wanted (missing or smaller: GDN2_ERR_WORKSPACE).
+ * Outputs and the workspace must not overlap inputs or each other.
+ */
+gdn2_status gdn2_qk_norm_rope_bwd(const void* q, const void* k, const float* weight_q, const float* weight_k,
+                                  const float* inv_freq, const int32_t* positions, const void* d_q_out,
+                                  const void* d_k_out, void* d_q, void* d_k, float* d_weight_q, float* d_weight_k,
+                                  int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t d, int32_t rot,
+                                  int32_t interleaved, float q_scale, float eps, gdn2_dtype dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Workspace of gdn2_qk_norm_rope_bwd: up to 1024 partial rows of 2 d FP32 sums.
+ * 0 for invalid sizes and without tokens. */
+size_t gdn2_qk_norm_rope_bwd_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t Hk, int32_t d);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* gdn2_status_string(gdn2_status status);
 
