@@ -42,12 +42,12 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kC = kLinearChunk;
+constexpr int kAuxOut = 2;  // buffer cache policy of the outputs' stores: nt
 
 // Waits for the wavefront's own LDS accesses and meets the others; its global
 // loads stay in flight.
@@ -71,39 +71,46 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes)
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) { return f32x2_to_bf16x2(a, b); }
 
-// LDS tiles of rows of D elements, in granules of 16 bytes whose place is
-// XORed with a linear map of the row's low four bits: 16-byte reads of
-// neighbouring rows at one granule, and the transposed reads below, then fall
-// into different banks.
+// LDS tiles of rows of D elements, in granules of 16 bytes whose place is XORed
+// with a linear map of the row's low four bits.  The maps keep free of bank
+// conflicts the 16-byte reads of 16 rows at four granules (the lanes of one access
+// cycle hold rows 0-3 and 12-15 at one granule and 4-11 at the next: the images of
+// rows 4 and 8 differ in bit 0 alone), the transposing reads of 16 columns of 16
+// rows (the images of rows 1, 2 and 4 differ in more than bit 0), and the stores
+// of four columns a lane.
 template <typename T, int D>
 struct Tile {
     static constexpr int kRow = D * int(sizeof(T));
     static constexpr int kGranules = kRow / 16;
     static constexpr __host__ __device__ int swz(int row)
     {
-        return kRow >= 256 ? (row ^ (((row >> 2) ^ (row >> 3)) & 1)) & 15 : kRow == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+        return kRow >= 256   ? ((row & 7) << 1) ^ (row & 8 ? 9 : 0)
+               : kRow == 128 ? (row & 6) ^ (row & 8 ? 5 : 0)
+                             : ((row & 4) >> 1) ^ (row & 8 ? 3 : 0);
     }
     static __device__ __forceinline__ int off(int row, int granule) { return row * kRow + ((granule ^ swz(row)) << 4); }
 };
 
-// An operand of a matrix product with 32 rows (or columns), one per lane & 31,
-// and an inner index that half-wavefront h = lane >> 5 takes its own part of.
-// bf16: 16 inner indices a product; FP32: 8, in four products of two.
-//   rows:  inner index along the tile's rows (the natural order)
-//   cols:  inner index down the tile's rows, 32 columns; order "accumulator":
-//          the rows {8 g + 4 h .. + 3} that a lane holds in a 32 x 32
-//          accumulator, so that `from_acc` of another tile is the other operand
+// An operand of a 16 x 16 matrix product: 16 rows (or columns), one per lane & 15,
+// and an inner index that quarter-wavefront g = lane >> 4 takes its own part of.
+// bf16: 32 inner indices a product; FP32: 16, in four products of four.
+//   rows:     inner index along a tile's rows (the natural order)
+//   cols:     inner index down a tile's rows, 16 columns; order "accumulator": of
+//             every 16 rows the four 4 g .. + 3 that a lane holds in a 16 x 16
+//             accumulator, so that
+//   from_acc: an accumulator tile is the other operand as it is.
 template <typename T>
 struct Frag;
 
 template <>
 struct Frag<bf16raw> {
-    static constexpr int kInner = 16;
+    static constexpr int kInner = 32, kTerms = 3, kAcc = 2;  // kAcc: accumulator tiles an operand takes
     bf16x8 x;
+    static __device__ __forceinline__ int inner(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
     template <int D>
-    static __device__ __forceinline__ Frag rows(const unsigned char* tile, int row, int s, int h)
+    static __device__ __forceinline__ Frag rows(const unsigned char* tile, int row0, int s, int lane)
     {
-        return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(tile + Tile<bf16raw, D>::off(row, 2 * s + h)))};
+        return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(tile + Tile<bf16raw, D>::off(row0 + (lane & 15), 4 * s + (lane >> 4))))};
     }
     // In each group of 16 lanes the transposing load takes four rows of 16
     // columns: lane 4 r + c reads columns 4 c .. + 3 of row r, and lane l
@@ -111,28 +118,23 @@ struct Frag<bf16raw> {
     template <int D>
     static __device__ __forceinline__ Frag cols(const unsigned char* tile, int col0, int s, int lane)
     {
-        const int h = lane >> 5, c = col0 + (lane & 16) + 4 * (lane & 3), r = 4 * h + ((lane & 15) >> 2);
+        const int c = col0 + 4 * (lane & 3), r = 4 * (lane >> 4) + ((lane & 15) >> 2);
         using TL = Tile<bf16raw, D>;
-        const int lo = TL::off(16 * s + r, c >> 3) + ((c & 4) << 1), hi = TL::off(16 * s + 8 + r, c >> 3) + ((c & 4) << 1);
+        const int lo = TL::off(32 * s + r, c >> 3) + ((c & 4) << 1), hi = TL::off(32 * s + 16 + r, c >> 3) + ((c & 4) << 1);
         const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(tile + lo));
         const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(tile + hi));
         return {__builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7))};
     }
-    static __device__ __forceinline__ Frag from_acc(const f32x16& p, int s)
+    static __device__ __forceinline__ Frag from_acc(const f32x4* p)
     {
-        const uint4 u = {pack2(p[8 * s], p[8 * s + 1]), pack2(p[8 * s + 2], p[8 * s + 3]), pack2(p[8 * s + 4], p[8 * s + 5]),
-                         pack2(p[8 * s + 6], p[8 * s + 7])};
-        return {__builtin_bit_cast(bf16x8, u)};
+        return {__builtin_bit_cast(bf16x8, make_uint4(pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]), pack2(p[1][0], p[1][1]),
+                                                      pack2(p[1][2], p[1][3])))};
     }
-    __device__ __forceinline__ f32x16 times(const Frag& b, f32x16 c) const
+    // Elements times `scale` as three bf16 terms, each the upper 16 bits of what
+    // the ones before leave: together all 24 bits.
+    __device__ __forceinline__ void split(const float* scale, Frag (&out)[3]) const
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, b.x, c, 0, 0, 0);
-    }
-    // this^T (b scaled): b's elements times `scale` as three bf16 terms, each the
-    // upper 16 bits of what the ones before leave.
-    __device__ __forceinline__ static void split(const Frag& b, const float* scale, Frag (&out)[3])
-    {
-        const uint4 u = __builtin_bit_cast(uint4, b.x);
+        const uint4 u = __builtin_bit_cast(uint4, x);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         uint32_t t[3][4];
 #pragma unroll
@@ -151,47 +153,44 @@ struct Frag<bf16raw> {
 #pragma unroll
         for (int k = 0; k < 3; ++k) out[k].x = __builtin_bit_cast(bf16x8, make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]));
     }
-    static constexpr int kTerms = 3;
+    __device__ __forceinline__ f32x4 times(const Frag& b, f32x4 c) const
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b.x, c, 0, 0, 0);
+    }
 };
 
 template <>
 struct Frag<float> {
-    static constexpr int kInner = 8;
+    static constexpr int kInner = 16, kTerms = 1, kAcc = 1;
     f32x4 x;
+    static __device__ __forceinline__ int inner(int e, int g) { return 4 * g + e; }
     template <int D>
-    static __device__ __forceinline__ Frag rows(const unsigned char* tile, int row, int s, int h)
+    static __device__ __forceinline__ Frag rows(const unsigned char* tile, int row0, int s, int lane)
     {
-        return {*reinterpret_cast<const f32x4*>(tile + Tile<float, D>::off(row, 2 * s + h))};
+        return {*reinterpret_cast<const f32x4*>(tile + Tile<float, D>::off(row0 + (lane & 15), 4 * s + (lane >> 4)))};
     }
     template <int D>
     static __device__ __forceinline__ Frag cols(const unsigned char* tile, int col0, int s, int lane)
     {
-        const int c = col0 + (lane & 31), r = 8 * s + 4 * (lane >> 5);
+        const int c = col0 + (lane & 15), r = 16 * s + 4 * (lane >> 4);
         Frag f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             f.x[e] = *reinterpret_cast<const float*>(tile + Tile<float, D>::off(r + e, c >> 2) + ((c & 3) << 2));
         return f;
     }
-    static __device__ __forceinline__ Frag from_acc(const f32x16& p, int s)
+    static __device__ __forceinline__ Frag from_acc(const f32x4* p) { return {p[0]}; }
+    __device__ __forceinline__ void split(const float* scale, Frag (&out)[1]) const
     {
-        return {f32x4{p[4 * s], p[4 * s + 1], p[4 * s + 2], p[4 * s + 3]}};
+        out[0].x = f32x4{x[0] * scale[0], x[1] * scale[1], x[2] * scale[2], x[3] * scale[3]};
     }
-    __device__ __forceinline__ f32x16 times(const Frag& b, f32x16 c) const
+    __device__ __forceinline__ f32x4 times(const Frag& b, f32x4 c) const
     {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], b.x[e], c, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], b.x[e], c, 0, 0, 0);
         return c;
     }
-    __device__ __forceinline__ static void split(const Frag& b, const float* scale, Frag (&out)[1])
-    {
-        out[0].x = f32x4{b.x[0] * scale[0], b.x[1] * scale[1], b.x[2] * scale[2], b.x[3] * scale[3]};
-    }
-    static constexpr int kTerms = 1;
 };
-
-// The row of a 32 x 32 accumulator that element r of a lane in half h holds.
-__device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
 // Four consecutive elements into LDS.
 __device__ __forceinline__ void put4(unsigned char* p, const float* v, bf16raw*)
@@ -201,36 +200,6 @@ __device__ __forceinline__ void put4(unsigned char* p, const float* v, bf16raw*)
 __device__ __forceinline__ void put4(unsigned char* p, const float* v, float*)
 {
     *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-}
-
-// 32 columns (rows of the accumulator) of one token: lane's 16 values to global
-// memory.  bf16: the two halves exchange groups of four, so that each lane stores
-// 16 contiguous bytes.
-__device__ __forceinline__ void store_row(rsrc_t r, uint32_t off, const f32x16& o, int h, bf16raw*)
-{
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2(o[2 * i], o[2 * i + 1]);
-    // groups g = 0..3 hold columns 8 g + 4 h .. + 3 (two words): lower half ends
-    // with columns 16 j .. + 7, upper half with 16 j + 8 .. + 15
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const auto a = __builtin_amdgcn_permlane32_swap(w[4 * j], w[4 * j + 2], false, false);
-        const auto b = __builtin_amdgcn_permlane32_swap(w[4 * j + 1], w[4 * j + 3], false, false);
-        typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-        const u32x4 v = {a[0], b[0], a[1], b[1]};
-        __builtin_amdgcn_raw_buffer_store_b128(v, r, int(off + 32 * j + 16 * h), 0, 0);
-    }
-}
-__device__ __forceinline__ void store_row(rsrc_t r, uint32_t off, const f32x16& o, int h, float*)
-{
-    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const u32x4 v = {__float_as_uint(o[4 * g]), __float_as_uint(o[4 * g + 1]), __float_as_uint(o[4 * g + 2]),
-                         __float_as_uint(o[4 * g + 3])};
-        __builtin_amdgcn_raw_buffer_store_b128(v, r, int(off + 32 * g + 16 * h), 0, 0);
-    }
 }
 
 // alpha as the other kernels take it: in [2^-15, 1], NaN as 2^-15.
@@ -259,17 +228,23 @@ __device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, in
     return n > 0 ? n - 1 : 0;
 }
 
+// A workgroup's wavefronts and LDS.  bf16 keeps two chunks in LDS, so that one is
+// staged while the other is used (one barrier a chunk); FP32 has room for one.
 template <typename T, int DA, int CW, bool OUT>
 struct Shape {
-    static constexpr int kOutWaves = OUT ? 2 * (CW / 32) : 0;
-    static constexpr int kStateTiles = (DA / 32) * (CW / 32);
-    static constexpr int kStateWaves = kStateTiles < 4 ? kStateTiles : 4;
-    static constexpr int kTiles = kStateTiles / kStateWaves;  // 32 x 32 tiles of X a state wavefront
+    static constexpr int kOutWaves = OUT ? 4 : 0;  // 16 tokens of a chunk each
+    static constexpr int kStateWaves = CW / 16;  // 16 columns of X each
+    static constexpr int kTiles = DA / 16;       // in tiles of 16 x 16
     static constexpr int kThreads = 64 * (kOutWaves + kStateWaves);
+    static constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     static constexpr int kBytesXY = kC * DA * int(sizeof(T)), kBytesZ = kC * CW * int(sizeof(T));
+    static constexpr int kBytesS = OUT ? CW * DA * int(sizeof(T)) : 0;
     static constexpr int kOffY = 0, kOffZ = kBytesXY, kOffX = kOffZ + kBytesZ;
-    static constexpr int kOffS = kOffX + (OUT ? kBytesXY : 0);
-    static constexpr int kOffPow = kOffS + (OUT ? CW * DA * int(sizeof(T)) : 0);
+    static constexpr int kBuf = kOffX + (OUT ? kBytesXY : 0);  // one chunk's tiles
+    static constexpr int kOffS = kBufs * kBuf;
+    static constexpr int kOffO = kOffS + kBufs * kBytesS;      // outputs on their way to memory
+    static constexpr int kBytesO = OUT ? kBytesZ : 0;
+    static constexpr int kOffPow = kOffO + kBufs * kBytesO;
     static constexpr int kLds = kOffPow + 80 * 4;
 };
 
@@ -327,20 +302,19 @@ struct Place {
 };
 
 // The chunks of a walk as one wavefront sees them: every wavefront stages its
-// share of the tiles; state wavefronts (STATER) keep X, the others form outputs.
-template <typename T, int DA, int CW, bool OUT, bool STATER>
+// share of the tiles; output wavefront ROLE forms the outputs of tokens 16 ROLE ..
+// + 15 of each chunk, state wavefronts (ROLE kState) keep X.
+constexpr int kState = 4;
+template <typename T, int DA, int CW, bool OUT, int ROLE>
 __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned char* lds, int tid)
 {
     using SH = Shape<T, DA, CW, OUT>;
     using F = Frag<T>;
-    constexpr int NT = SH::kThreads, EB = int(sizeof(T)), CB = CW / 32, TS = SH::kTiles;
-    constexpr int kSteps = kC / F::kInner, kPer = F::kInner / 2;   // inner indices a lane takes a step
-    unsigned char* const lY = lds + SH::kOffY;
-    unsigned char* const lZ = lds + SH::kOffZ;
-    unsigned char* const lX = lds + SH::kOffX;
-    unsigned char* const lS = lds + SH::kOffS;
+    constexpr bool STATER = ROLE == kState;
+    constexpr int NT = SH::kThreads, EB = int(sizeof(T)), TS = SH::kTiles;
+    constexpr int kSteps = kC / F::kInner, kPer = F::kInner / 4;   // inner indices a lane takes a step
     float* const pw = reinterpret_cast<float*>(lds + SH::kOffPow);
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, l = lane & 15;
     const bool back = pl.w.back;
     const int late = back ? 1 : 0;
 
@@ -353,57 +327,72 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     const int64_t zoff = ((pl.row0 * a.H + pl.hd) * a.width + pl.col0) * EB;
     const char* const pz = static_cast<const char*>(pl.w.z) + zoff;
 
-    Stage<T, DA, NT> sx, sy;
-    Stage<T, CW, NT> sz;
-    const auto fetch = [&](int64_t t0, int n) {
+    // Chunk c of the walk, c = 0 .. chunks - 1: its tokens are loaded into registers
+    // a chunk before they are staged in LDS.
+    struct Staged {
+        Stage<T, DA, NT> x, y;
+        Stage<T, CW, NT> z;
+    };
+    Staged st;
+    const int chunks = (pl.left + kC - 1) / kC;
+    const auto length = [&](int c) { return c + 1 < chunks ? kC : pl.left - c * kC; };
+    const auto first = [&](int c) { return back ? pl.tok - int64_t(c) * kC - length(c) : pl.tok + int64_t(c) * kC; };
+    const auto fetch = [&](int c, Staged& g) {
+        const int n = length(c);
+        const int64_t t0 = first(c);
         const rsrc_t ry = make_rsrc(py + t0 * strideA, uint32_t(n - 1) * strideA + DA * EB);
         const rsrc_t rz = make_rsrc(pz + t0 * strideZ, uint32_t(n - 1) * strideZ + CW * EB);
-        sy.load(ry, strideA, n, back, tid);
-        sz.load(rz, strideZ, n, back, tid);
+        g.y.load(ry, strideA, n, back, tid);
+        g.z.load(rz, strideZ, n, back, tid);
         if (OUT) {
             const rsrc_t rx = make_rsrc(px + t0 * strideA, uint32_t(n - 1) * strideA + DA * EB);
-            sx.load(rx, strideA, n, back, tid);
+            g.x.load(rx, strideA, n, back, tid);
         }
     };
-    int64_t tok = pl.tok;
-    int left = pl.left, L = left < kC ? left : kC;
-    if (left > 0) fetch(back ? tok - L : tok, L);
+    const auto stage = [&](const Staged& g, unsigned char* buf) {
+        g.y.store(buf + SH::kOffY, tid);
+        g.z.store(buf + SH::kOffZ, tid);
+        if (OUT) g.x.store(buf + SH::kOffX, tid);
+    };
+    if (chunks > 0) fetch(0, st);
     lds_barrier();  // pw
 
-    const int sw = wave - SH::kOutWaves;
-    const int ih = wave & 1, cb = STATER ? sw % CB : wave >> 1, db0 = STATER ? sw / CB * TS : 0;
+    // State wavefronts: columns 16 cb .., this lane column 16 cb + l and rows
+    // 16 t + 4 g + r of tile t.
+    const int cb = STATER ? wave - SH::kOutWaves : 0;
 
-    // Constants of the head: output wavefronts hold the decays of their diagonal
-    // and lower tile and of the carry's read, state wavefronts those of their z.
-    float dec[2][16], read = 0.f, scale[kSteps * kPer];
+    // Constants of the head: output wavefronts hold the decays of their tiles of P
+    // (by the distance of the tile's tokens) and of the carry's read, state
+    // wavefronts those of their z.
+    float dec[4][4], read = 0.f, scale[kSteps * kPer];
     const auto scales = [&](int n) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                const int j = s * F::kInner + 8 * (e >> 2) + 4 * h + (e & 3), at = n - 1 + late - j;
+                const int at = n - 1 + late - (s * F::kInner + F::inner(e, g));
                 scale[s * kPer + e] = pw[at < 0 ? 0 : at];
             }
     };
-    f32x16 X[TS];
+    f32x4 X[TS];
     if constexpr (!STATER) {
-        const int i = lane & 31;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int j = acc_row(r, h);
-            dec[0][r] = pw[i >= j ? i - j : 0];
-            dec[1][r] = pw[32 + i - j];
-        }
-        read = pw[32 * ih + i + 1 - late];
+        for (int dt = 0; dt <= ROLE; ++dt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int apart = 16 * dt + l - (4 * g + r);
+                dec[dt][r] = pw[apart < 0 ? 0 : apart];
+            }
+        read = pw[16 * ROLE + l + 1 - late];
     } else {
-        scales(L);
+        scales(chunks > 0 ? length(0) : kC);
         // the carry: what comes in, or the segments before this one in order
 #pragma unroll
         for (int t = 0; t < TS; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) X[t][r] = 0.f;
+            for (int r = 0; r < 4; ++r) X[t][r] = 0.f;
         const int64_t sd = pl.w.state_d, square = int64_t(DA) * a.width;
-        const int64_t c = (pl.col0 + 32 * cb + (lane & 31)) * int64_t(pl.w.state_c);
+        const int64_t c = (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
         if (pl.w.carry_in && pl.m == 0) {
             // Where there are several segments, the launch for carries leaves what comes in
             // in the slot of the last one, which has no carry to keep: the last segment may
@@ -415,8 +404,8 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t at = (32 * (db0 + t) + acc_row(r, h)) * sd;
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t at = (16 * t + 4 * g + r) * sd;
                     X[t][r] = p[at];
                     if (!OUT) keep[at] = X[t][r];
                 }
@@ -428,87 +417,146 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
                 for (int t = 0; t < TS; ++t)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) X[t][r] = over * X[t][r] + p[(32 * (db0 + t) + acc_row(r, h)) * sd];
+                    for (int r = 0; r < 4; ++r) X[t][r] = over * X[t][r] + p[(16 * t + 4 * g + r) * sd];
         }
     }
 
-    while (left > 0) {
-        sy.store(lY, tid);
-        sz.store(lZ, tid);
-        if (OUT) sx.store(lX, tid);
+    // X as the output wavefronts read it
+    const auto publish = [&](unsigned char* lS) {
         if constexpr (OUT && STATER) {
 #pragma unroll
-            for (int t = 0; t < TS; ++t)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int d = 32 * (db0 + t) + 8 * g + 4 * h, per = 16 / EB;
-                    const float v[4] = {X[t][4 * g], X[t][4 * g + 1], X[t][4 * g + 2], X[t][4 * g + 3]};
-                    put4(lS + Tile<T, DA>::off(32 * cb + (lane & 31), d / per) + (d % per) * EB, v, static_cast<T*>(nullptr));
-                }
-        }
-        const int L1 = left - L < kC ? left - L : kC;
-        const int64_t t0 = back ? tok - L : tok, t1 = back ? t0 - L1 : t0 + L;
-        if (L1 > 0) fetch(t1, L1);
-        lds_barrier();
-        if constexpr (!STATER) {
-            F xf[DA / F::kInner];
-            f32x16 o;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] = 0.f;
-#pragma unroll
-            for (int s = 0; s < DA / F::kInner; ++s) {
-                xf[s] = F::template rows<DA>(lX, 32 * ih + (lane & 31), s, h);
-                o = F::template rows<DA>(lS, 32 * cb + (lane & 31), s, h).times(xf[s], o);
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] *= read;
-#pragma unroll
-            for (int jb = 0; jb < 2; ++jb) {
-                if (jb > ih) break;
-                f32x16 p;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) p[r] = 0.f;
-#pragma unroll
-                for (int s = 0; s < DA / F::kInner; ++s)
-                    p = F::template rows<DA>(lY, 32 * jb + (lane & 31), s, h).times(xf[s], p);
-                if (jb == ih) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) p[r] = acc_row(r, h) <= (lane & 31) ? p[r] * dec[0][r] : 0.f;
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) p[r] *= dec[1][r];
-                }
-#pragma unroll
-                for (int s = 0; s < 32 / F::kInner; ++s)
-                    o = F::template cols<CW>(lZ, 32 * cb, 32 / F::kInner * jb + s, lane).times(F::from_acc(p, s), o);
-            }
-            const rsrc_t ro = make_rsrc(static_cast<char*>(pl.w.out) + zoff + t0 * strideZ, uint32_t(L - 1) * strideZ + CW * EB);
-            const int i = 32 * ih + (lane & 31);
-            const uint32_t off = i < L ? uint32_t(back ? L - 1 - i : i) * strideZ + 32 * cb * EB : 0x80000000u;
-            store_row(ro, off, o, h, static_cast<T*>(nullptr));
-        } else {
-            if (L < kC) scales(L);
-            const float over = pw[L];
-#pragma unroll
-            for (int t = 0; t < TS; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) X[t][r] *= over;
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                F z[F::kTerms];
-                F::split(F::template cols<CW>(lZ, 32 * cb, s, lane), scale + s * kPer, z);
-#pragma unroll
-                for (int t = 0; t < TS; ++t) {
-                    const F y = F::template cols<DA>(lY, 32 * (db0 + t), s, lane);
-#pragma unroll
-                    for (int k = F::kTerms - 1; k >= 0; --k) X[t] = y.times(z[k], X[t]);
-                }
+            for (int t = 0; t < TS; ++t) {
+                const int d = 16 * t + 4 * g, per = 16 / EB;
+                const float v[4] = {X[t][0], X[t][1], X[t][2], X[t][3]};
+                put4(lS + Tile<T, DA>::off(16 * cb + l, d / per) + (d % per) * EB, v, static_cast<T*>(nullptr));
             }
         }
+    };
+    const auto outputs = [&](const unsigned char* buf, const unsigned char* lS, unsigned char* lO) {
+        const unsigned char* const lY = buf + SH::kOffY;
+        const unsigned char* const lZ = buf + SH::kOffZ;
+        const unsigned char* const lX = buf + SH::kOffX;
+        constexpr int ND = DA / F::kInner, NC = CW / 16, NP = ROLE + 1;       // tiles of P: the tokens up to ROLE's
+        constexpr int NJ = (NP + F::kAcc - 1) / F::kAcc;                        // operands that they make
+        F xf[ND];
+        f32x4 p[NJ * F::kAcc], o[NC];
+#pragma unroll
+        for (int s = 0; s < ND; ++s) xf[s] = F::template rows<DA>(lX, 16 * ROLE, s, lane);
+#pragma unroll
+        for (int t = 0; t < NJ * F::kAcc; ++t) {
+            p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (t >= NP) continue;
+#pragma unroll
+            for (int s = 0; s < ND; ++s) p[t] = F::template rows<DA>(lY, 16 * t, s, lane).times(xf[s], p[t]);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < ND; ++s) o[c] = F::template rows<DA>(lS, 16 * c, s, lane).times(xf[s], o[c]);
+        }
+#pragma unroll
+        for (int t = 0; t < NP; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                p[t][r] *= dec[ROLE - t][r];
+                if (t == ROLE) p[t][r] = 4 * g + r <= l ? p[t][r] : 0.f;
+            }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[c][r] *= read;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                o[c] = F::template cols<CW>(lZ, 16 * c, j, lane).times(F::from_acc(p + j * F::kAcc), o[c]);
+            const int col = 16 * c + 4 * g, per = 16 / EB;
+            const float v[4] = {o[c][0], o[c][1], o[c][2], o[c][3]};
+            put4(lO + Tile<T, CW>::off(16 * ROLE + l, col / per) + (col % per) * EB, v, static_cast<T*>(nullptr));
+        }
+    };
+    // A chunk's outputs from LDS to memory, whole rows of the slice at a time (stored
+    // straight from the accumulators, 32 bytes of a row at once, they took 17 us of
+    // 132 us without any product).
+    const auto flush = [&](int c, const unsigned char* lO) {
+        if constexpr (OUT) {
+            constexpr int kG = Tile<T, CW>::kGranules, kTotal = kC * kG;
+            const int n = length(c);
+            const rsrc_t ro = make_rsrc(static_cast<char*>(pl.w.out) + zoff + first(c) * strideZ, uint32_t(n - 1) * strideZ + CW * EB);
+#pragma unroll
+            for (int i = 0; i < (kTotal + NT - 1) / NT; ++i) {
+                const int at = tid + i * NT, row = at / kG;
+                if (kTotal % NT && at >= kTotal) break;
+                typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+                const u32x4 v = *reinterpret_cast<const u32x4*>(lO + Tile<T, CW>::off(row, at % kG));
+                const uint32_t off = uint32_t(back ? n - 1 - row : row) * strideZ + uint32_t(at % kG) * 16;
+                __builtin_amdgcn_raw_buffer_store_b128(v, ro, int(row < n ? off : 0x80000000u), 0, kAuxOut);
+            }
+        }
+    };
+    const auto update = [&](int c, const unsigned char* buf) {
+        const int n = length(c);
+        if (n < kC) scales(n);
+        const float over = pw[n];
+#pragma unroll
+        for (int t = 0; t < TS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) X[t][r] *= over;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            F z[F::kTerms];
+            F::template cols<CW>(buf + SH::kOffZ, 16 * cb, s, lane).split(scale + s * kPer, z);
+#pragma unroll
+            for (int t = 0; t < TS; ++t) {
+                const F y = F::template cols<DA>(buf + SH::kOffY, 16 * t, s, lane);
+#pragma unroll
+                for (int k = F::kTerms - 1; k >= 0; --k) X[t] = y.times(z[k], X[t]);
+            }
+        }
+    };
+
+    unsigned char* const lS = lds + SH::kOffS;
+    unsigned char* const lO = lds + SH::kOffO;
+    if constexpr (SH::kBufs == 1) {
+        for (int c = 0; c < chunks; ++c) {
+            stage(st, lds);
+            publish(lS);
+            if (c > 0) flush(c - 1, lO);
+            if (c + 1 < chunks) fetch(c + 1, st);
+            lds_barrier();
+            if constexpr (STATER) update(c, lds);
+            else outputs(lds, lS, lO);
+            lds_barrier();
+        }
+        if (chunks > 0) flush(chunks - 1, lO);
+    } else if (chunks > 0) {
+        // While chunk c is used from buffers c & 1, chunk c + 1 goes from registers to
+        // the other ones, c + 2 is on its way into the registers, and the outputs of
+        // c - 1 leave.
+        stage(st, lds);
+        publish(lS);
+        if (chunks > 1) fetch(1, st);
         lds_barrier();
-        tok = back ? t0 : t0 + L;
-        left -= L;
-        L = L1;
+        const auto turn = [&](int c, unsigned char* buf, unsigned char* other, unsigned char* s0, unsigned char* s1,
+                              unsigned char* o0, unsigned char* o1) {
+            if (c > 0) flush(c - 1, o1);
+            if constexpr (STATER) {
+                update(c, buf);
+                if (c + 1 < chunks) publish(s1);
+            } else {
+                outputs(buf, s0, o0);
+            }
+            if (c + 1 < chunks) stage(st, other);
+            if (c + 2 < chunks) fetch(c + 2, st);
+            lds_barrier();
+        };
+        unsigned char* const b1 = lds + SH::kBuf;
+        unsigned char* const lS1 = lS + SH::kBytesS;
+        unsigned char* const lO1 = lO + SH::kBytesO;
+        for (int c = 0; c < chunks; c += 2) {
+            turn(c, lds, b1, lS, lS1, lO, lO1);
+            if (c + 1 < chunks) turn(c + 1, b1, lds, lS1, lS, lO1, lO);
+        }
+        flush(chunks - 1, (chunks & 1) ? lO : lO1);
     }
 
     if constexpr (STATER) {
@@ -516,17 +564,17 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         if (out) {
             const int64_t square = int64_t(DA) * a.width;
             float* p = out + ((OUT ? int64_t(pl.n) : pl.slot) * a.H + pl.hd) * square +
-                       (pl.col0 + 32 * cb + (lane & 31)) * int64_t(pl.w.state_c);
+                       (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) p[(32 * (db0 + t) + acc_row(r, h)) * int64_t(pl.w.state_d)] = X[t][r];
+                for (int r = 0; r < 4; ++r) p[(16 * t + 4 * g + r) * int64_t(pl.w.state_d)] = X[t][r];
         }
     }
 }
 
 template <typename T, int DA, int CW, bool OUT>
-__global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) void walk_kernel(LinearLaunch a)
+__global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) __attribute__((amdgpu_waves_per_eu(1, 2))) void walk_kernel(LinearLaunch a)
 {
     using SH = Shape<T, DA, CW, OUT>;
     __shared__ __attribute__((aligned(16))) unsigned char lds[SH::kLds];
@@ -563,10 +611,14 @@ __global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) void walk_kernel
     pl.row0 = brow * a.T;
     pl.tok = pl.w.back ? eos - before : bos + before;
 
-    if (__builtin_amdgcn_readfirstlane(tid >> 6) < SH::kOutWaves)
-        walk<T, DA, CW, OUT, false>(a, pl, lds, tid);
-    else
-        walk<T, DA, CW, OUT, true>(a, pl, lds, tid);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (wave >= SH::kOutWaves) return walk<T, DA, CW, OUT, kState>(a, pl, lds, tid);
+    if constexpr (OUT) {
+        if (wave == 0) walk<T, DA, CW, OUT, 0>(a, pl, lds, tid);
+        else if (wave == 1) walk<T, DA, CW, OUT, 1>(a, pl, lds, tid);
+        else if (wave == 2) walk<T, DA, CW, OUT, 2>(a, pl, lds, tid);
+        else walk<T, DA, CW, OUT, 3>(a, pl, lds, tid);
+    }
 }
 
 template <typename T, int DA, int CW, bool OUT>
