@@ -723,14 +723,14 @@ gdn2_status linear_attn_fwd(const void* q, const void* k, const void* v, const f
                                     {span_or_none(final_state, st), span_or_none(o, nv),
                                      span_or_none(p.carry_bytes ? workspace : nullptr, int64_t(p.carry_bytes))}, 0, 4))
         return s;
-    const bool bf16 = dtype == GDN2_DTYPE_BF16;
+    const bool bf16 = dtype == GDN2_DTYPE_BF16, exact = final_state != nullptr;
     gdn2::LinearLaunch a = linear_launch(alpha, cu_seqlens, B, T, H, N, p, zero_padding);
     a.walks = 1;
     a.width = dv;
     a.walk[0] = {q, k, v, o, initial_state, final_state, static_cast<float*>(p.carry_bytes ? workspace : nullptr), dv, 1, 0};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = p.segments > 1 ? gdn2::launch_linear_walk(a, dk, true, bf16, s) : hipSuccess;
-    if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, bf16, s);
+    hipError_t e = p.segments > 1 ? gdn2::launch_linear_walk(a, dk, true, exact, bf16, s) : hipSuccess;
+    if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, exact, bf16, s);
     return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
 }
 
@@ -762,7 +762,7 @@ gdn2_status linear_attn_bwd(const void* q, const void* k, const void* v, const f
                                      span_or_none(d_initial_state, st),
                                      span_or_none(need ? workspace : nullptr, int64_t(need))}))
         return s;
-    const bool bf16 = dtype == GDN2_DTYPE_BF16;
+    const bool bf16 = dtype == GDN2_DTYPE_BF16, exact = d_initial_state != nullptr;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     float* const carry_s = static_cast<float*>(need ? workspace : nullptr);
     float* const carry_r = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.carry_bytes) : nullptr;
@@ -774,7 +774,7 @@ gdn2_status linear_attn_bwd(const void* q, const void* k, const void* v, const f
         a.width = dv;
         a.walk[0] = {nullptr, k, v, nullptr, initial_state, nullptr, carry_s, dv, 1, 0};
         a.walk[1] = {nullptr, q, d_o, nullptr, d_final_state, nullptr, carry_r, dv, 1, 1};
-        e = gdn2::launch_linear_walk(a, dk, true, bf16, s);
+        e = gdn2::launch_linear_walk(a, dk, true, exact, bf16, s);
     }
     const gdn2::LinearWalk to_k{v, d_o, q, dk_, d_final_state, nullptr, carry_r, 1, dv, 1};
     const gdn2::LinearWalk to_v{k, q, d_o, dv_, d_final_state, d_initial_state, carry_r, dv, 1, 1};
@@ -785,15 +785,15 @@ gdn2_status linear_attn_bwd(const void* q, const void* k, const void* v, const f
         a.walk[1] = to_v;
         a.walk[2] = to_q;
         a.walks = 3;
-        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, bf16, s);
+        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, exact, bf16, s);
     } else {
         a.walk[1] = to_q;
         a.walks = 2;
-        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dv, false, bf16, s);
+        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dv, false, false, bf16, s);
         a.walk[0] = to_v;
         a.walks = 1;
         a.width = dv;
-        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, bf16, s);
+        if (e == hipSuccess) e = gdn2::launch_linear_walk(a, dk, false, exact, bf16, s);
     }
     return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP;
 }

@@ -321,7 +321,8 @@ int64_t qk_rope_bwd_partials(int64_t tokens, int32_t heads_q, int32_t heads_k, i
 // Each returns hipSuccess or the launch error; bf16 selects the input dtype.
 hipError_t launch_qk_rope(QkRopeArgs a, bool bf16, hipStream_t stream);
 hipError_t launch_qk_rope_bwd(QkRopeBwdArgs a, bool bf16, hipStream_t stream);
-hipError_t launch_linear_walk(const LinearLaunch& a, int da, bool carries_only, bool bf16, hipStream_t stream);
+// exact: the carries are those of FP32 arithmetic (the caller gets one of them).
+hipError_t launch_linear_walk(const LinearLaunch& a, int da, bool carries_only, bool exact, bool bf16, hipStream_t stream);
 hipError_t launch_linear_step(const LinearStepArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream);
 hipError_t launch_dropout(const DropoutCall& a, bool bf16, hipStream_t stream);

@@ -30,10 +30,11 @@
 // head: each lane keeps its own in registers for the whole walk.
 //
 // Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  P and the
-// copy of X that the outputs read are rounded to bf16, as the outputs are (both
-// far below the rounding of sums of such products to bf16 outputs: 2^-9 rms
-// each); X itself is not: a^n z is split into three bf16 terms that hold all 24
-// bits, so the carry is that of FP32 arithmetic.
+// copy of X that the outputs read are rounded to bf16, as the outputs are: each
+// adds to an output what its own rounding does.  X itself is FP32.  Where the
+// caller gets it, the factor a^n z of its update goes in as three bf16 terms that
+// hold all 24 bits, so that it is the state of FP32 arithmetic; where only the
+// bf16 copy is read, as two (2^-17).
 #include "gdn2_device.hpp"
 #include "launch.hpp"
 
@@ -104,7 +105,8 @@ struct Frag;
 
 template <>
 struct Frag<bf16raw> {
-    static constexpr int kInner = 32, kTerms = 3, kAcc = 2;  // kAcc: accumulator tiles an operand takes
+    static constexpr int kInner = 32, kAcc = 2;  // kAcc: accumulator tiles an operand takes
+    static constexpr int terms(bool exact) { return exact ? 3 : 2; }
     bf16x8 x;
     static __device__ __forceinline__ int inner(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
     template <int D>
@@ -130,28 +132,28 @@ struct Frag<bf16raw> {
         return {__builtin_bit_cast(bf16x8, make_uint4(pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]), pack2(p[1][0], p[1][1]),
                                                       pack2(p[1][2], p[1][3])))};
     }
-    // Elements times `scale` as three bf16 terms, each the upper 16 bits of what
-    // the ones before leave: together all 24 bits.
-    __device__ __forceinline__ void split(const float* scale, Frag (&out)[3]) const
+    // Elements times `scale` as N bf16 terms, each the upper 16 bits of what the
+    // ones before leave (three hold all 24 bits), the last one rounded.
+    template <int N>
+    __device__ __forceinline__ void split(const float* scale, Frag (&out)[N]) const
     {
         const uint4 u = __builtin_bit_cast(uint4, x);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t t[3][4];
+        uint32_t t[N][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float lo = __uint_as_float(w[i] << 16) * scale[2 * i], hi = __uint_as_float(w[i] & 0xffff0000u) * scale[2 * i + 1];
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
+            for (int k = 0; k < N - 1; ++k) {
                 const uint32_t ul = __float_as_uint(lo), uh = __float_as_uint(hi);
                 t[k][i] = __builtin_amdgcn_perm(uh, ul, 0x07060302);  // the upper halves
-                if (k < 2) {
-                    lo -= __uint_as_float(ul & 0xffff0000u);
-                    hi -= __uint_as_float(uh & 0xffff0000u);
-                }
+                lo -= __uint_as_float(ul & 0xffff0000u);
+                hi -= __uint_as_float(uh & 0xffff0000u);
             }
+            t[N - 1][i] = pack2(lo, hi);
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) out[k].x = __builtin_bit_cast(bf16x8, make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]));
+        for (int k = 0; k < N; ++k) out[k].x = __builtin_bit_cast(bf16x8, make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]));
     }
     __device__ __forceinline__ f32x4 times(const Frag& b, f32x4 c) const
     {
@@ -161,7 +163,8 @@ struct Frag<bf16raw> {
 
 template <>
 struct Frag<float> {
-    static constexpr int kInner = 16, kTerms = 1, kAcc = 1;
+    static constexpr int kInner = 16, kAcc = 1;
+    static constexpr int terms(bool) { return 1; }
     f32x4 x;
     static __device__ __forceinline__ int inner(int e, int g) { return 4 * g + e; }
     template <int D>
@@ -180,7 +183,8 @@ struct Frag<float> {
         return f;
     }
     static __device__ __forceinline__ Frag from_acc(const f32x4* p) { return {p[0]}; }
-    __device__ __forceinline__ void split(const float* scale, Frag (&out)[1]) const
+    template <int N>
+    __device__ __forceinline__ void split(const float* scale, Frag (&out)[N]) const
     {
         out[0].x = f32x4{x[0] * scale[0], x[1] * scale[1], x[2] * scale[2], x[3] * scale[3]};
     }
@@ -202,10 +206,22 @@ __device__ __forceinline__ void put4(unsigned char* p, const float* v, float*)
     *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
 }
 
+// alpha^n for a whole n >= 0, by squaring in 64 bits: off by n 2^-53, far below FP32.
 // alpha as the other kernels take it: in [2^-15, 1], NaN as 2^-15.
-__device__ __forceinline__ double log2_alpha(float alpha)
+__device__ __forceinline__ float power(float alpha, uint32_t n)
 {
-    return log2(double(fminf(fmaxf(alpha, 0x1p-15f), 1.0f)));
+    double a = double(fminf(fmaxf(alpha, 0x1p-15f), 1.0f)), p = 1.0;
+    for (; n; n >>= 1, a *= a)
+        if (n & 1) p *= a;
+    return float(p);
+}
+// The same for n <= 64.
+__device__ __forceinline__ float small_power(float alpha, int n)
+{
+    double a = double(fminf(fmaxf(alpha, 0x1p-15f), 1.0f)), p = 1.0;
+#pragma unroll
+    for (int b = 0; b < 7; ++b, a *= a) p = n >> b & 1 ? p * a : p;
+    return float(p);
 }
 
 // Segment m of sequence n in [0, slots): slot = start / seg_len + n + m, which
@@ -305,7 +321,7 @@ struct Place {
 // share of the tiles; output wavefront ROLE forms the outputs of tokens 16 ROLE ..
 // + 15 of each chunk, state wavefronts (ROLE kState) keep X.
 constexpr int kState = 4;
-template <typename T, int DA, int CW, bool OUT, int ROLE>
+template <typename T, int DA, int CW, bool OUT, bool EXACT, int ROLE>
 __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned char* lds, int tid)
 {
     using SH = Shape<T, DA, CW, OUT>;
@@ -319,8 +335,6 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     const int late = back ? 1 : 0;
 
     const float al = a.alpha[pl.hd];
-    for (int i = tid; i <= kC; i += NT) pw[i] = float(exp2(log2_alpha(al) * i));
-
     const uint32_t strideA = uint32_t(a.H) * DA * EB, strideZ = uint32_t(a.H) * a.width * EB;
     const char* const px = static_cast<const char*>(pl.w.x) + (pl.row0 * a.H + pl.hd) * DA * EB;
     const char* const py = static_cast<const char*>(pl.w.y) + (pl.row0 * a.H + pl.hd) * DA * EB;
@@ -355,6 +369,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         if (OUT) g.x.store(buf + SH::kOffX, tid);
     };
     if (chunks > 0) fetch(0, st);
+    for (int i = tid; i <= kC; i += NT) pw[i] = small_power(al, i);
     lds_barrier();  // pw
 
     // State wavefronts: columns 16 cb .., this lane column 16 cb + l and rows
@@ -411,13 +426,30 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
                 }
         }
         if (OUT && pl.m > 0) {
-            const float over = float(exp2(log2_alpha(al) * a.seg_len));
-            const float* p = pl.w.segment_carry + ((pl.slot - pl.m) * a.H + pl.hd) * square + c;
-            for (int j = 0; j < pl.m; ++j, p += a.H * square)
+            // two segments' carries on their way at a time (one: 0.85 us a segment; four
+            // spill); behind the last one it is read again and has no weight
+            const float over = power(al, uint32_t(a.seg_len));
+            const float* const p = pl.w.segment_carry + ((pl.slot - pl.m) * a.H + pl.hd) * square + c;
+            for (int j = 0; j < pl.m; j += 2) {
+                const bool two = j + 1 < pl.m;
+                const float* const p0 = p + j * a.H * square;
+                const float* const p1 = two ? p0 + a.H * square : p0;
+                f32x4 v[2][TS];
 #pragma unroll
                 for (int t = 0; t < TS; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) X[t][r] = over * X[t][r] + p[(16 * t + 4 * g + r) * sd];
+                    for (int r = 0; r < 4; ++r) {
+                        v[0][t][r] = p0[(16 * t + 4 * g + r) * sd];
+                        v[1][t][r] = p1[(16 * t + 4 * g + r) * sd];
+                    }
+#pragma unroll
+                for (int t = 0; t < TS; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        X[t][r] = over * X[t][r] + v[0][t][r];
+                        if (two) X[t][r] = over * X[t][r] + v[1][t][r];
+                    }
+            }
         }
     }
 
@@ -503,13 +535,14 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
             for (int r = 0; r < 4; ++r) X[t][r] *= over;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            F z[F::kTerms];
+            constexpr int kTerms = F::terms(EXACT);
+            F z[kTerms];
             F::template cols<CW>(buf + SH::kOffZ, 16 * cb, s, lane).split(scale + s * kPer, z);
 #pragma unroll
             for (int t = 0; t < TS; ++t) {
                 const F y = F::template cols<DA>(buf + SH::kOffY, 16 * t, s, lane);
 #pragma unroll
-                for (int k = F::kTerms - 1; k >= 0; --k) X[t] = y.times(z[k], X[t]);
+                for (int k = kTerms - 1; k >= 0; --k) X[t] = y.times(z[k], X[t]);
             }
         }
     };
@@ -573,7 +606,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     }
 }
 
-template <typename T, int DA, int CW, bool OUT>
+template <typename T, int DA, int CW, bool OUT, bool EXACT>
 __global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) __attribute__((amdgpu_waves_per_eu(1, 2))) void walk_kernel(LinearLaunch a)
 {
     using SH = Shape<T, DA, CW, OUT>;
@@ -612,42 +645,47 @@ __global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) __attribute__((a
     pl.tok = pl.w.back ? eos - before : bos + before;
 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    if (wave >= SH::kOutWaves) return walk<T, DA, CW, OUT, kState>(a, pl, lds, tid);
+    if (wave >= SH::kOutWaves) return walk<T, DA, CW, OUT, EXACT, kState>(a, pl, lds, tid);
     if constexpr (OUT) {
-        if (wave == 0) walk<T, DA, CW, OUT, 0>(a, pl, lds, tid);
-        else if (wave == 1) walk<T, DA, CW, OUT, 1>(a, pl, lds, tid);
-        else if (wave == 2) walk<T, DA, CW, OUT, 2>(a, pl, lds, tid);
-        else walk<T, DA, CW, OUT, 3>(a, pl, lds, tid);
+        if (wave == 0) walk<T, DA, CW, OUT, EXACT, 0>(a, pl, lds, tid);
+        else if (wave == 1) walk<T, DA, CW, OUT, EXACT, 1>(a, pl, lds, tid);
+        else if (wave == 2) walk<T, DA, CW, OUT, EXACT, 2>(a, pl, lds, tid);
+        else walk<T, DA, CW, OUT, EXACT, 3>(a, pl, lds, tid);
     }
 }
 
 template <typename T, int DA, int CW, bool OUT>
-hipError_t launch_shape(LinearLaunch a, hipStream_t stream)
+hipError_t launch_shape(LinearLaunch a, bool exact, hipStream_t stream)
 {
     a.walk_blocks = (a.units + 7) / 8 * 8 * (a.width / CW) * a.walks;
     const int64_t blocks = a.walk_blocks + (OUT ? a.pad_blocks : 0);
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((walk_kernel<T, DA, CW, OUT>), dim3(unsigned(blocks)), dim3(Shape<T, DA, CW, OUT>::kThreads), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(Shape<T, DA, CW, OUT>::kThreads);
+    if (exact || sizeof(T) == 4)
+        hipLaunchKernelGGL((walk_kernel<T, DA, CW, OUT, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((walk_kernel<T, DA, CW, OUT, sizeof(T) == 4>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 
 template <typename T, bool OUT>
-hipError_t launch_typed(const LinearLaunch& a, int da, hipStream_t stream)
+hipError_t launch_typed(const LinearLaunch& a, int da, bool exact, hipStream_t stream)
 {
     const bool wide = a.width % 64 == 0;
-    if (da == 32) return wide ? launch_shape<T, 32, 64, OUT>(a, stream) : launch_shape<T, 32, 32, OUT>(a, stream);
-    if (da == 64) return wide ? launch_shape<T, 64, 64, OUT>(a, stream) : launch_shape<T, 64, 32, OUT>(a, stream);
-    if (da == 128) return wide ? launch_shape<T, 128, 64, OUT>(a, stream) : launch_shape<T, 128, 32, OUT>(a, stream);
+    if (da == 32) return wide ? launch_shape<T, 32, 64, OUT>(a, exact, stream) : launch_shape<T, 32, 32, OUT>(a, exact, stream);
+    if (da == 64) return wide ? launch_shape<T, 64, 64, OUT>(a, exact, stream) : launch_shape<T, 64, 32, OUT>(a, exact, stream);
+    if (da == 128) return wide ? launch_shape<T, 128, 64, OUT>(a, exact, stream) : launch_shape<T, 128, 32, OUT>(a, exact, stream);
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_linear_walk(const LinearLaunch& a, int da, bool carries_only, bool bf16, hipStream_t stream)
+hipError_t launch_linear_walk(const LinearLaunch& a, int da, bool carries_only, bool exact, bool bf16, hipStream_t stream)
 {
     if (a.units == 0) return hipSuccess;
-    if (carries_only) return bf16 ? launch_typed<bf16raw, false>(a, da, stream) : launch_typed<float, false>(a, da, stream);
-    return bf16 ? launch_typed<bf16raw, true>(a, da, stream) : launch_typed<float, true>(a, da, stream);
+    if (carries_only)
+        return bf16 ? launch_typed<bf16raw, false>(a, da, exact, stream) : launch_typed<float, false>(a, da, exact, stream);
+    return bf16 ? launch_typed<bf16raw, true>(a, da, exact, stream) : launch_typed<float, true>(a, da, exact, stream);
 }
 
 }  // namespace gdn2
