@@ -48,6 +48,7 @@ typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kC = kLinearChunk;
+constexpr int kMayCross = 0x6;  // of a scheduling barrier: vector and scalar arithmetic
 constexpr int kAuxOut = 2;  // buffer cache policy of the outputs' stores: nt
 
 // Waits for the wavefront's own LDS accesses and meets the others; its global
@@ -470,37 +471,53 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         const unsigned char* const lX = buf + SH::kOffX;
         constexpr int ND = DA / F::kInner, NC = CW / 16, NP = ROLE + 1;       // tiles of P: the tokens up to ROLE's
         constexpr int NJ = (NP + F::kAcc - 1) / F::kAcc;                        // operands that they make
-        F xf[ND];
+        // The products with x: tiles of Y (16 tokens each) for P, then tiles of the
+        // carry (16 columns each).  Operands are read kAhead tiles before their
+        // matrix instructions; left to itself the compiler reads each where it is
+        // used, and the wavefront waits for LDS forty times a chunk.
+        constexpr int kTiles = NP + NC, kAhead = ND >= 8 ? 1 : 8 / ND, kZ = NC * NJ;
+        F xf[ND], fr[kAhead + 1][ND], zf[kZ];
         f32x4 p[NJ * F::kAcc], o[NC];
+        const auto load = [&](int k) {
+#pragma unroll
+            for (int s = 0; s < ND; ++s)
+                fr[k % (kAhead + 1)][s] = k < NP ? F::template rows<DA>(lY, 16 * k, s, lane) : F::template rows<DA>(lS, 16 * (k - NP), s, lane);
+        };
 #pragma unroll
         for (int s = 0; s < ND; ++s) xf[s] = F::template rows<DA>(lX, 16 * ROLE, s, lane);
 #pragma unroll
-        for (int t = 0; t < NJ * F::kAcc; ++t) {
-            p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (t >= NP) continue;
+        for (int k = 0; k < kAhead && k < kTiles; ++k) load(k);
+        if constexpr (NJ * F::kAcc > NP) p[NP] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < ND; ++s) p[t] = F::template rows<DA>(lY, 16 * t, s, lane).times(xf[s], p[t]);
-        }
+        for (int k = 0; k < kTiles; ++k) {
+            if (k + kAhead < kTiles) load(k + kAhead);
+            if (k == kTiles - 1) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < ND; ++s) o[c] = F::template rows<DA>(lS, 16 * c, s, lane).times(xf[s], o[c]);
-        }
-#pragma unroll
-        for (int t = 0; t < NP; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                p[t][r] *= dec[ROLE - t][r];
-                if (t == ROLE) p[t][r] = 4 * g + r <= l ? p[t][r] : 0.f;
+                for (int j = 0; j < kZ; ++j) zf[j] = F::template cols<CW>(lZ, 16 * (j / NJ), j % NJ, lane);
             }
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(kMayCross);
+            f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < ND; ++s) acc = fr[k % (kAhead + 1)][s].times(xf[s], acc);
+            if (k < NP) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    acc[r] *= dec[k < NP ? ROLE - k : 0][r];
+                    if (k == ROLE) acc[r] = 4 * g + r <= l ? acc[r] : 0.f;
+                }
+                p[k] = acc;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[k - NP][r] = acc[r] * read;
+            }
+        }
+        F pf[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) pf[j] = F::from_acc(p + j * F::kAcc);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o[c][r] *= read;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                o[c] = F::template cols<CW>(lZ, 16 * c, j, lane).times(F::from_acc(p + j * F::kAcc), o[c]);
+            for (int j = 0; j < NJ; ++j) o[c] = zf[c * NJ + j].times(pf[j], o[c]);
             const int col = 16 * c + 4 * g, per = 16 / EB;
             const float v[4] = {o[c][0], o[c][1], o[c][2], o[c][3]};
             put4(lO + Tile<T, CW>::off(16 * ROLE + l, col / per) + (col % per) * EB, v, static_cast<T*>(nullptr));
