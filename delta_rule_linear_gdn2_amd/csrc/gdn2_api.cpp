@@ -630,7 +630,7 @@ struct LinearPlan {
     size_t carry_bytes = 0;  // one state per slot and head
 };
 
-int32_t linear_slices(int32_t width) { return width % 64 == 0 ? width / 64 : 1; }
+int32_t linear_slices(int32_t width, int32_t da, bool bf16) { return width / gdn2::linear_slice(width, da, bf16); }
 
 LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, int32_t subs, int32_t cus)
 {
@@ -663,14 +663,15 @@ bool linear_sizes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32
            tokens_ok(num_seqs, 1, H) && tokens_ok(B, 1, H) && supported_head(dk) && supported_head(dv);
 }
 
-LinearPlan linear_fwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs)
+LinearPlan linear_fwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, gdn2_dtype dtype)
 {
-    return linear_plan(B, T, H, dk, dv, num_seqs, linear_slices(dv), device_cus());
+    return linear_plan(B, T, H, dk, dv, num_seqs, linear_slices(dv, dk, dtype == GDN2_DTYPE_BF16), device_cus());
 }
 
-LinearPlan linear_bwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs)
+LinearPlan linear_bwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, gdn2_dtype dtype)
 {
-    return linear_plan(B, T, H, dk, dv, num_seqs, 2 * linear_slices(dk) + linear_slices(dv), device_cus());
+    const bool bf16 = dtype == GDN2_DTYPE_BF16;
+    return linear_plan(B, T, H, dk, dv, num_seqs, 2 * linear_slices(dk, dv, bf16) + linear_slices(dv, dk, bf16), device_cus());
 }
 
 gdn2::LinearLaunch linear_launch(const float* alpha, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t N,
@@ -709,7 +710,7 @@ gdn2_status linear_attn_fwd(const void* q, const void* k, const void* v, const f
     const int32_t N = cu_seqlens ? num_seqs : B;
     if (T > 0 && (!q || !k || !v || !o)) return GDN2_ERR_NULL_POINTER;
     if (misaligned({q, k, v, o, initial_state, final_state, workspace})) return GDN2_ERR_MISALIGNED;
-    LinearPlan p = linear_fwd_plan(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0);
+    LinearPlan p = linear_fwd_plan(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0, dtype);
     if (!workspace && p.carry_bytes) {  // one segment a sequence
         p = LinearPlan{};
         p.seg_len = T;
@@ -745,7 +746,7 @@ gdn2_status linear_attn_bwd(const void* q, const void* k, const void* v, const f
     if (T > 0 && (!q || !k || !v || !d_o || !dq || !dk_ || !dv_)) return GDN2_ERR_NULL_POINTER;
     if (misaligned({q, k, v, d_o, initial_state, d_final_state, dq, dk_, dv_, d_initial_state, workspace}))
         return GDN2_ERR_MISALIGNED;
-    LinearPlan p = linear_bwd_plan(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0);
+    LinearPlan p = linear_bwd_plan(B, T, H, dk, dv, cu_seqlens ? num_seqs : 0, dtype);
     if (!workspace && p.carry_bytes) {
         p = LinearPlan{};
         p.seg_len = T;
@@ -1247,8 +1248,7 @@ gdn2_status gdn2_linear_attn_fwd(const void* q, const void* k, const void* v, co
 size_t gdn2_linear_attn_fwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs,
                                             gdn2_dtype dtype)
 {
-    (void)dtype;
-    return linear_sizes(B, T, H, dk, dv, num_seqs) ? linear_fwd_plan(B, T, H, dk, dv, num_seqs).carry_bytes : 0;
+    return linear_sizes(B, T, H, dk, dv, num_seqs) ? linear_fwd_plan(B, T, H, dk, dv, num_seqs, dtype).carry_bytes : 0;
 }
 
 gdn2_status gdn2_linear_attn_bwd(const void* q, const void* k, const void* v, const float* alpha,
@@ -1265,9 +1265,8 @@ gdn2_status gdn2_linear_attn_bwd(const void* q, const void* k, const void* v, co
 size_t gdn2_linear_attn_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk_size, int32_t dv_size,
                                             int32_t num_seqs, gdn2_dtype dtype)
 {
-    (void)dtype;
     return linear_sizes(B, T, H, dk_size, dv_size, num_seqs)
-               ? 2 * linear_bwd_plan(B, T, H, dk_size, dv_size, num_seqs).carry_bytes
+               ? 2 * linear_bwd_plan(B, T, H, dk_size, dv_size, num_seqs, dtype).carry_bytes
                : 0;
 }
 

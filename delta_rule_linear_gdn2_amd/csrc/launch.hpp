@@ -250,6 +250,9 @@ struct ColumnSumArgs {
 // Linear attention with a fixed decay for each head, as walks (see
 // linear_attn.hip): x, y [B, T, H, DA], z and out [B, T, H, width].
 constexpr int kLinearChunk = 64;
+// Columns a workgroup walks: 64 where they divide the width, but 32 for FP32 rows x,
+// y of 128, whose tiles fill the LDS.
+inline int linear_slice(int width, int da, bool bf16) { return width % 64 == 0 && (bf16 || da < 128) ? 64 : 32; }
 struct LinearWalk {
     const void* x;        // null in a launch for carries only
     const void* y;

@@ -45,6 +45,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kC = kLinearChunk;
@@ -93,27 +94,50 @@ struct Tile {
     static __device__ __forceinline__ int off(int row, int granule) { return row * kRow + ((granule ^ swz(row)) << 4); }
 };
 
-// An operand of a 16 x 16 matrix product: 16 rows (or columns), one per lane & 15,
-// and an inner index that quarter-wavefront g = lane >> 4 takes its own part of.
-// bf16: 32 inner indices a product; FP32: 16, in four products of four.
+// FP32 values as the sum of three bf16 ones, each the upper 16 bits of what the
+// ones before leave: together all 24 bits.  (An infinity leaves a NaN behind it.)
+template <int N>
+__device__ __forceinline__ void split_pair(float lo, float hi, uint32_t (&t)[N])
+{
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k) {
+        const uint32_t ul = __float_as_uint(lo), uh = __float_as_uint(hi);
+        t[k] = __builtin_amdgcn_perm(uh, ul, 0x07060302);  // the upper halves
+        lo -= __uint_as_float(ul & 0xffff0000u);
+        hi -= __uint_as_float(uh & 0xffff0000u);
+    }
+    t[N - 1] = pack2(lo, hi);
+}
+
+// Planes of bf16 that hold the elements of type T.
+template <typename T>
+constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
+
+// An operand of a 16 x 16 matrix product over 32 inner indices: 16 rows (or
+// columns), one per lane & 15, and of the inner indices eight a quarter-wavefront
+// g = lane >> 4.
 //   rows:     inner index along a tile's rows (the natural order)
 //   cols:     inner index down a tile's rows, 16 columns; order "accumulator": of
 //             every 16 rows the four 4 g .. + 3 that a lane holds in a 16 x 16
 //             accumulator, so that
-//   from_acc: an accumulator tile is the other operand as it is.
+//   from_acc: two accumulator tiles are the other operand as they are.
+// FP32 operands are three bf16 planes, and a product six: what is left out is
+// 2^-24 of it.  (The FP32 matrix instructions take 2.7 times as long.)
 template <typename T>
-struct Frag;
-
-template <>
-struct Frag<bf16raw> {
-    static constexpr int kInner = 32, kAcc = 2;  // kAcc: accumulator tiles an operand takes
-    static constexpr int terms(bool exact) { return exact ? 3 : 2; }
-    bf16x8 x;
+struct Frag {
+    static constexpr int PL = kPlanes<T>;
+    bf16x8 x[PL];
     static __device__ __forceinline__ int inner(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
-    template <int D>
+    template <int D, int ROWS>
     static __device__ __forceinline__ Frag rows(const unsigned char* tile, int row0, int s, int lane)
     {
-        return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(tile + Tile<bf16raw, D>::off(row0 + (lane & 15), 4 * s + (lane >> 4))))};
+        using TL = Tile<bf16raw, D>;
+        Frag f;
+#pragma unroll
+        for (int k = 0; k < PL; ++k)
+            f.x[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(tile + k * ROWS * TL::kRow +
+                                                                               TL::off(row0 + (lane & 15), 4 * s + (lane >> 4))));
+        return f;
     }
     // In each group of 16 lanes the transposing load takes four rows of 16
     // columns: lane 4 r + c reads columns 4 c .. + 3 of row r, and lane l
@@ -121,90 +145,130 @@ struct Frag<bf16raw> {
     template <int D>
     static __device__ __forceinline__ Frag cols(const unsigned char* tile, int col0, int s, int lane)
     {
-        const int c = col0 + 4 * (lane & 3), r = 4 * (lane >> 4) + ((lane & 15) >> 2);
         using TL = Tile<bf16raw, D>;
+        const int c = col0 + 4 * (lane & 3), r = 4 * (lane >> 4) + ((lane & 15) >> 2);
         const int lo = TL::off(32 * s + r, c >> 3) + ((c & 4) << 1), hi = TL::off(32 * s + 16 + r, c >> 3) + ((c & 4) << 1);
-        const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(tile + lo));
-        const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(tile + hi));
-        return {__builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7))};
+        Frag f;
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+            const unsigned char* const t = tile + k * kC * TL::kRow;
+            const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + lo));
+            const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(t + hi));
+            f.x[k] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        return f;
+    }
+    __device__ __forceinline__ void put(int pair, const uint32_t (&t)[PL])
+    {
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+            u32x4 u = __builtin_bit_cast(u32x4, x[k]);
+            u[pair] = t[k];
+            x[k] = __builtin_bit_cast(bf16x8, u);
+        }
     }
     static __device__ __forceinline__ Frag from_acc(const f32x4* p)
     {
-        return {__builtin_bit_cast(bf16x8, make_uint4(pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]), pack2(p[1][0], p[1][1]),
-                                                      pack2(p[1][2], p[1][3])))};
-    }
-    // Elements times `scale` as N bf16 terms, each the upper 16 bits of what the
-    // ones before leave (three hold all 24 bits), the last one rounded.
-    template <int N>
-    __device__ __forceinline__ void split(const float* scale, Frag (&out)[N]) const
-    {
-        const uint4 u = __builtin_bit_cast(uint4, x);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t t[N][4];
+        Frag f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo = __uint_as_float(w[i] << 16) * scale[2 * i], hi = __uint_as_float(w[i] & 0xffff0000u) * scale[2 * i + 1];
-#pragma unroll
-            for (int k = 0; k < N - 1; ++k) {
-                const uint32_t ul = __float_as_uint(lo), uh = __float_as_uint(hi);
-                t[k][i] = __builtin_amdgcn_perm(uh, ul, 0x07060302);  // the upper halves
-                lo -= __uint_as_float(ul & 0xffff0000u);
-                hi -= __uint_as_float(uh & 0xffff0000u);
-            }
-            t[N - 1][i] = pack2(lo, hi);
+            uint32_t t[PL];
+            split_pair<PL>(p[i >> 1][2 * (i & 1)], p[i >> 1][2 * (i & 1) + 1], t);
+            f.put(i, t);
         }
+        return f;
+    }
+    // The elements as FP32.
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
 #pragma unroll
-        for (int k = 0; k < N; ++k) out[k].x = __builtin_bit_cast(bf16x8, make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]));
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = v[2 * i + 1] = 0.f;
+#pragma unroll
+            for (int k = PL - 1; k >= 0; --k) {
+                const uint32_t u = __builtin_bit_cast(u32x4, x[k])[i];
+                v[2 * i] = k == PL - 1 ? __uint_as_float(u << 16) : v[2 * i] + __uint_as_float(u << 16);
+                v[2 * i + 1] = k == PL - 1 ? __uint_as_float(u & 0xffff0000u) : v[2 * i + 1] + __uint_as_float(u & 0xffff0000u);
+            }
+        }
     }
     __device__ __forceinline__ f32x4 times(const Frag& b, f32x4 c) const
     {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b.x, c, 0, 0, 0);
+        if constexpr (PL == 3) {
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[2], b.x[0], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], b.x[2], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], b.x[1], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], b.x[0], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], b.x[1], c, 0, 0, 0);
+        }
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], b.x[0], c, 0, 0, 0);
     }
 };
 
-template <>
-struct Frag<float> {
-    static constexpr int kInner = 16, kAcc = 1;
-    static constexpr int terms(bool) { return 1; }
-    f32x4 x;
-    static __device__ __forceinline__ int inner(int e, int g) { return 4 * g + e; }
-    template <int D>
-    static __device__ __forceinline__ Frag rows(const unsigned char* tile, int row0, int s, int lane)
+// The factor of the carry's update, z times its decays.  FP32: three planes like
+// any operand.  bf16: N terms, of which the other operand (one plane) takes each.
+template <typename T, bool EXACT>
+struct Scaled;
+
+template <bool EXACT>
+struct Scaled<float, EXACT> {
+    Frag<float> f;
+    __device__ __forceinline__ Scaled(const Frag<float>& z, const float* scale)
     {
-        return {*reinterpret_cast<const f32x4*>(tile + Tile<float, D>::off(row0 + (lane & 15), 4 * s + (lane >> 4)))};
-    }
-    template <int D>
-    static __device__ __forceinline__ Frag cols(const unsigned char* tile, int col0, int s, int lane)
-    {
-        const int c = col0 + (lane & 15), r = 16 * s + 4 * (lane >> 4);
-        Frag f;
+        float v[8];
+        z.get(v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            f.x[e] = *reinterpret_cast<const float*>(tile + Tile<float, D>::off(r + e, c >> 2) + ((c & 3) << 2));
-        return f;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t t[3];
+            split_pair<3>(v[2 * i] * scale[2 * i], v[2 * i + 1] * scale[2 * i + 1], t);
+            f.put(i, t);
+        }
     }
-    static __device__ __forceinline__ Frag from_acc(const f32x4* p) { return {p[0]}; }
-    template <int N>
-    __device__ __forceinline__ void split(const float* scale, Frag (&out)[N]) const
+    __device__ __forceinline__ f32x4 times(const Frag<float>& y, f32x4 c) const { return y.times(f, c); }
+};
+
+template <bool EXACT>
+struct Scaled<bf16raw, EXACT> {
+    static constexpr int N = EXACT ? 3 : 2;
+    Frag<bf16raw> f[N];
+    __device__ __forceinline__ Scaled(const Frag<bf16raw>& z, const float* scale)
     {
-        out[0].x = f32x4{x[0] * scale[0], x[1] * scale[1], x[2] * scale[2], x[3] * scale[3]};
+        float v[8];
+        z.get(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t t[N];
+            split_pair<N>(v[2 * i] * scale[2 * i], v[2 * i + 1] * scale[2 * i + 1], t);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const uint32_t one[1] = {t[k]};
+                f[k].put(i, one);
+            }
+        }
     }
-    __device__ __forceinline__ f32x4 times(const Frag& b, f32x4 c) const
+    __device__ __forceinline__ f32x4 times(const Frag<bf16raw>& y, f32x4 c) const
     {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], b.x[e], c, 0, 0, 0);
+        for (int k = N - 1; k >= 0; --k) c = y.times(f[k], c);
         return c;
     }
 };
 
-// Four consecutive elements into LDS.
-__device__ __forceinline__ void put4(unsigned char* p, const float* v, bf16raw*)
+// Four consecutive elements into LDS: as they are, and as operand planes `stride`
+// bytes apart.
+__device__ __forceinline__ void put4(unsigned char* p, const f32x4& v, bf16raw*)
 {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
-__device__ __forceinline__ void put4(unsigned char* p, const float* v, float*)
+__device__ __forceinline__ void put4(unsigned char* p, const f32x4& v, float*) { *reinterpret_cast<f32x4*>(p) = v; }
+template <int PL>
+__device__ __forceinline__ void put4_planes(unsigned char* p, int stride, const f32x4& v)
 {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    uint32_t a[PL], b[PL];
+    split_pair<PL>(v[0], v[1], a);
+    split_pair<PL>(v[2], v[3], b);
+#pragma unroll
+    for (int k = 0; k < PL; ++k) *reinterpret_cast<uint2*>(p + k * stride) = make_uint2(a[k], b[k]);
 }
 
 // alpha^n for a whole n >= 0, by squaring in 64 bits: off by n 2^-53, far below FP32.
@@ -246,7 +310,8 @@ __device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, in
 }
 
 // A workgroup's wavefronts and LDS.  bf16 keeps two chunks in LDS, so that one is
-// staged while the other is used (one barrier a chunk); FP32 has room for one.
+// staged while the other is used (one barrier a chunk); FP32, with three planes,
+// has room for one.
 template <typename T, int DA, int CW, bool OUT>
 struct Shape {
     static constexpr int kOutWaves = OUT ? 4 : 0;  // 16 tokens of a chunk each
@@ -254,42 +319,58 @@ struct Shape {
     static constexpr int kTiles = DA / 16;       // in tiles of 16 x 16
     static constexpr int kThreads = 64 * (kOutWaves + kStateWaves);
     static constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
-    static constexpr int kBytesXY = kC * DA * int(sizeof(T)), kBytesZ = kC * CW * int(sizeof(T));
-    static constexpr int kBytesS = OUT ? CW * DA * int(sizeof(T)) : 0;
+    static constexpr int PL = kPlanes<T>;
+    static constexpr int kBytesXY = PL * kC * DA * 2, kBytesZ = PL * kC * CW * 2;
+    static constexpr int kBytesS = OUT ? PL * CW * DA * 2 : 0;
     static constexpr int kOffY = 0, kOffZ = kBytesXY, kOffX = kOffZ + kBytesZ;
     static constexpr int kBuf = kOffX + (OUT ? kBytesXY : 0);  // one chunk's tiles
     static constexpr int kOffS = kBufs * kBuf;
     static constexpr int kOffO = kOffS + kBufs * kBytesS;      // outputs on their way to memory
-    static constexpr int kBytesO = OUT ? kBytesZ : 0;
+    static constexpr int kBytesO = OUT ? kC * CW * int(sizeof(T)) : 0;
     static constexpr int kOffPow = kOffO + kBufs * kBytesO;
     static constexpr int kLds = kOffPow + 80 * 4;
 };
 
-// One thread's granules of a chunk's tile of `rows` of D elements.
+// One thread's share of a chunk's tile of kC rows of D elements, in groups of eight.
 template <typename T, int D, int THREADS>
 struct Stage {
-    static constexpr int kG = Tile<T, D>::kGranules, kTotal = kC * kG, kN = (kTotal + THREADS - 1) / THREADS;
-    uint4 v[kN];
+    static constexpr int kG = D / 8, kTotal = kC * kG, kN = (kTotal + THREADS - 1) / THREADS, kWide = int(sizeof(T)) / 2;
+    u32x4 v[kN][kWide];
     __device__ __forceinline__ void load(rsrc_t r, uint32_t stride, int L, bool back, int tid)
     {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int g = tid + i * THREADS;
-            if (kTotal % THREADS && g >= kTotal) break;
-            const int row = g / kG;
-            const uint32_t off = uint32_t(back ? L - 1 - row : row) * stride + uint32_t(g % kG) * 16;
+            const int at = tid + i * THREADS;
+            if (kTotal % THREADS && at >= kTotal) break;
+            const int row = at / kG;
+            const uint32_t off = uint32_t(back ? L - 1 - row : row) * stride + uint32_t(at % kG) * (16 * kWide);
             // a row behind the last one (before the first one, walking back) is past the window
-            const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, int(row < L ? off : 0x80000000u), 0, 0);
-            v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int j = 0; j < kWide; ++j)
+                v[i][j] = __builtin_amdgcn_raw_buffer_load_b128(r, int(row < L ? off + 16 * j : 0x80000000u), 0, 0);
         }
     }
     __device__ __forceinline__ void store(unsigned char* tile, int tid) const
     {
+        using TL = Tile<bf16raw, D>;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int g = tid + i * THREADS;
-            if (kTotal % THREADS && g >= kTotal) break;
-            *reinterpret_cast<uint4*>(tile + Tile<T, D>::off(g / kG, g % kG)) = v[i];
+            const int at = tid + i * THREADS;
+            if (kTotal % THREADS && at >= kTotal) break;
+            unsigned char* const p = tile + TL::off(at / kG, at % kG);
+            if constexpr (kWide == 1) {
+                *reinterpret_cast<u32x4*>(p) = v[i][0];
+            } else {
+                u32x4 out[3];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t t[3];
+                    split_pair<3>(__uint_as_float(v[i][j >> 1][2 * (j & 1)]), __uint_as_float(v[i][j >> 1][2 * (j & 1) + 1]), t);
+                    out[0][j] = t[0], out[1][j] = t[1], out[2][j] = t[2];
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4*>(p + k * kC * TL::kRow) = out[k];
+            }
         }
     }
 };
@@ -329,7 +410,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     using F = Frag<T>;
     constexpr bool STATER = ROLE == kState;
     constexpr int NT = SH::kThreads, EB = int(sizeof(T)), TS = SH::kTiles;
-    constexpr int kSteps = kC / F::kInner, kPer = F::kInner / 4;   // inner indices a lane takes a step
+    constexpr int kSteps = kC / 32, kPer = 8;   // products over a chunk's tokens, tokens a lane takes in each
     float* const pw = reinterpret_cast<float*>(lds + SH::kOffPow);
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, l = lane & 15;
     const bool back = pl.w.back;
@@ -386,7 +467,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                const int at = n - 1 + late - (s * F::kInner + F::inner(e, g));
+                const int at = n - 1 + late - (32 * s + F::inner(e, g));
                 scale[s * kPer + e] = pw[at < 0 ? 0 : at];
             }
     };
@@ -459,9 +540,8 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         if constexpr (OUT && STATER) {
 #pragma unroll
             for (int t = 0; t < TS; ++t) {
-                const int d = 16 * t + 4 * g, per = 16 / EB;
-                const float v[4] = {X[t][0], X[t][1], X[t][2], X[t][3]};
-                put4(lS + Tile<T, DA>::off(16 * cb + l, d / per) + (d % per) * EB, v, static_cast<T*>(nullptr));
+                const int d = 16 * t + 4 * g;
+                put4_planes<SH::PL>(lS + Tile<bf16raw, DA>::off(16 * cb + l, d >> 3) + ((d & 4) << 1), CW * DA * 2, X[t]);
             }
         }
     };
@@ -469,25 +549,26 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         const unsigned char* const lY = buf + SH::kOffY;
         const unsigned char* const lZ = buf + SH::kOffZ;
         const unsigned char* const lX = buf + SH::kOffX;
-        constexpr int ND = DA / F::kInner, NC = CW / 16, NP = ROLE + 1;       // tiles of P: the tokens up to ROLE's
-        constexpr int NJ = (NP + F::kAcc - 1) / F::kAcc;                        // operands that they make
+        constexpr int ND = DA / 32, NC = CW / 16, NP = ROLE + 1;  // tiles of P: the tokens up to ROLE's
+        constexpr int NJ = (NP + 1) / 2;                          // operands that they make
         // The products with x: tiles of Y (16 tokens each) for P, then tiles of the
         // carry (16 columns each).  Operands are read kAhead tiles before their
         // matrix instructions; left to itself the compiler reads each where it is
         // used, and the wavefront waits for LDS forty times a chunk.
-        constexpr int kTiles = NP + NC, kAhead = ND >= 8 ? 1 : 8 / ND, kZ = NC * NJ;
+        constexpr int kTiles = NP + NC, kAhead = 8 / (ND * SH::PL), kZ = NC * NJ;
         F xf[ND], fr[kAhead + 1][ND], zf[kZ];
-        f32x4 p[NJ * F::kAcc], o[NC];
+        f32x4 p[2 * NJ], o[NC];
         const auto load = [&](int k) {
 #pragma unroll
             for (int s = 0; s < ND; ++s)
-                fr[k % (kAhead + 1)][s] = k < NP ? F::template rows<DA>(lY, 16 * k, s, lane) : F::template rows<DA>(lS, 16 * (k - NP), s, lane);
+                fr[k % (kAhead + 1)][s] = k < NP ? F::template rows<DA, kC>(lY, 16 * k, s, lane)
+                                                 : F::template rows<DA, CW>(lS, 16 * (k - NP), s, lane);
         };
 #pragma unroll
-        for (int s = 0; s < ND; ++s) xf[s] = F::template rows<DA>(lX, 16 * ROLE, s, lane);
+        for (int s = 0; s < ND; ++s) xf[s] = F::template rows<DA, kC>(lX, 16 * ROLE, s, lane);
 #pragma unroll
         for (int k = 0; k < kAhead && k < kTiles; ++k) load(k);
-        if constexpr (NJ * F::kAcc > NP) p[NP] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (2 * NJ > NP) p[NP] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < kTiles; ++k) {
             if (k + kAhead < kTiles) load(k + kAhead);
@@ -495,7 +576,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
                 for (int j = 0; j < kZ; ++j) zf[j] = F::template cols<CW>(lZ, 16 * (j / NJ), j % NJ, lane);
             }
-            if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(kMayCross);
+            __builtin_amdgcn_sched_barrier(kMayCross);
             f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < ND; ++s) acc = fr[k % (kAhead + 1)][s].times(xf[s], acc);
@@ -513,14 +594,13 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         }
         F pf[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) pf[j] = F::from_acc(p + j * F::kAcc);
+        for (int j = 0; j < NJ; ++j) pf[j] = F::from_acc(p + 2 * j);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) o[c] = zf[c * NJ + j].times(pf[j], o[c]);
             const int col = 16 * c + 4 * g, per = 16 / EB;
-            const float v[4] = {o[c][0], o[c][1], o[c][2], o[c][3]};
-            put4(lO + Tile<T, CW>::off(16 * ROLE + l, col / per) + (col % per) * EB, v, static_cast<T*>(nullptr));
+            put4(lO + Tile<T, CW>::off(16 * ROLE + l, col / per) + (col % per) * EB, o[c], static_cast<T*>(nullptr));
         }
     };
     // A chunk's outputs from LDS to memory, whole rows of the slice at a time (stored
@@ -535,7 +615,6 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
             for (int i = 0; i < (kTotal + NT - 1) / NT; ++i) {
                 const int at = tid + i * NT, row = at / kG;
                 if (kTotal % NT && at >= kTotal) break;
-                typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
                 const u32x4 v = *reinterpret_cast<const u32x4*>(lO + Tile<T, CW>::off(row, at % kG));
                 const uint32_t off = uint32_t(back ? n - 1 - row : row) * strideZ + uint32_t(at % kG) * 16;
                 __builtin_amdgcn_raw_buffer_store_b128(v, ro, int(row < n ? off : 0x80000000u), 0, kAuxOut);
@@ -552,15 +631,9 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
             for (int r = 0; r < 4; ++r) X[t][r] *= over;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            constexpr int kTerms = F::terms(EXACT);
-            F z[kTerms];
-            F::template cols<CW>(buf + SH::kOffZ, 16 * cb, s, lane).split(scale + s * kPer, z);
+            const Scaled<T, EXACT> z(F::template cols<CW>(buf + SH::kOffZ, 16 * cb, s, lane), scale + s * kPer);
 #pragma unroll
-            for (int t = 0; t < TS; ++t) {
-                const F y = F::template cols<DA>(buf + SH::kOffY, 16 * t, s, lane);
-#pragma unroll
-                for (int k = kTerms - 1; k >= 0; --k) X[t] = y.times(z[k], X[t]);
-            }
+            for (int t = 0; t < TS; ++t) X[t] = z.times(F::template cols<DA>(buf + SH::kOffY, 16 * t, s, lane), X[t]);
         }
     };
 
@@ -688,10 +761,12 @@ hipError_t launch_shape(LinearLaunch a, bool exact, hipStream_t stream)
 template <typename T, bool OUT>
 hipError_t launch_typed(const LinearLaunch& a, int da, bool exact, hipStream_t stream)
 {
-    const bool wide = a.width % 64 == 0;
+    const bool wide = linear_slice(a.width, da, sizeof(T) == 2) == 64;
     if (da == 32) return wide ? launch_shape<T, 32, 64, OUT>(a, exact, stream) : launch_shape<T, 32, 32, OUT>(a, exact, stream);
     if (da == 64) return wide ? launch_shape<T, 64, 64, OUT>(a, exact, stream) : launch_shape<T, 64, 32, OUT>(a, exact, stream);
-    if (da == 128) return wide ? launch_shape<T, 128, 64, OUT>(a, exact, stream) : launch_shape<T, 128, 32, OUT>(a, exact, stream);
+    if constexpr (sizeof(T) == 2)
+        if (da == 128 && wide) return launch_shape<T, 128, 64, OUT>(a, exact, stream);
+    if (da == 128) return launch_shape<T, 128, 32, OUT>(a, exact, stream);
     return hipErrorInvalidValue;
 }
 
