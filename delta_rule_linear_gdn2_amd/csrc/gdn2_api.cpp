@@ -617,13 +617,8 @@ gdn2_status mixer_prologue_bwd(const void* const (&x)[3], const float* const (&c
 constexpr int32_t kLinearMaxHeads = 1 << 15;  // a chunk's rows stay inside the 32 bits of a buffer offset
 
 // Segments of the walks over sequences, and what their carries take.  A walk is
-// one workgroup per (segment, head, column slice, walk); `subs` of them share a
-// segment and head.
-//   batch:  as many segments a row as fill the compute units once, none shorter
-//           than four chunks
-//   packed: the lengths are on the device.  Segments of the share that each
-//           compute unit has of the whole, so that one long sequence does not
-//           outlast all others.
+// one workgroup per (segment, head, column slice, walk), one a compute unit at a
+// time; more than one segment a sequence takes a launch more, for their carries.
 struct LinearPlan {
     int32_t seg_len = 0, segments = 1;
     int64_t slots = 0;
@@ -632,23 +627,56 @@ struct LinearPlan {
 
 int32_t linear_slices(int32_t width, int32_t da, bool bf16) { return width / gdn2::linear_slice(width, da, bf16); }
 
-LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, int32_t subs, int32_t cus)
+// What the plan needs to know of a call: its workgroups per (sequence, head), in the
+// launch for outputs and in the one for carries.
+struct LinearShape {
+    int32_t subs, carry_subs, widest;
+    bool bf16;
+};
+
+// Microseconds that a call over B H groups of `chunks` chunks takes in P segments,
+// as measured on MI355X for small calls: a workgroup's start and end 5, a chunk
+// 1.0 to 1.6 (bf16) or 2.4 to 4.5 (FP32) with heads up to 64 or of 128, reading a
+// segment's carry 0.5, the launch for carries 7 and half a walk's slots.  In one
+// piece / by this rule: 4096 tokens of 16 heads of 128 forward 102 / 42, 1024 tokens
+// 29 / 21, 16384 tokens of 2 heads 390 / 57; 512 tokens 17.1 / in two chunks 17.8.
+double linear_cost(int64_t groups, int64_t chunks, int64_t P, const LinearShape& sh, int64_t cus)
 {
-    constexpr int64_t kShortest = 4 * gdn2::kLinearChunk;
+    const double chunk = sh.bf16 ? (sh.widest < 128 ? 1.0 : 1.5) : (sh.widest < 128 ? 2.4 : 4.5);
+    const double walk = chunk * double((chunks + P - 1) / P);
+    const double rounds = double((groups * sh.subs * P + cus - 1) / cus);
+    if (P == 1) return rounds * (5 + walk);
+    const double carry_rounds = double((groups * sh.carry_subs * (P - 1) + 2 * cus - 1) / (2 * cus));
+    return rounds * (5 + walk) + 0.5 * double(P - 1) + 7 + carry_rounds * walk;
+}
+
+LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, const LinearShape& sh,
+                       int32_t cus)
+{
+    constexpr int64_t kMost = 64;  // segments a row
+    const int64_t rows = num_seqs > 0 ? num_seqs : B, chunk = gdn2::kLinearChunk, chunks = (int64_t(T) + chunk - 1) / chunk;
     LinearPlan p;
-    const int64_t rows = num_seqs > 0 ? num_seqs : B;
     p.seg_len = T > 0 ? T : 1;
     p.slots = rows;
-    const int64_t groups = int64_t(num_seqs > 0 ? 1 : B) * H * subs;  // workgroups that walk T tokens
-    int64_t len;
+    int64_t len = T;
     if (num_seqs > 0) {
+        // The lengths are on the device.  Segments of a compute unit's share of the
+        // whole, none under four chunks (FP32: two); but where the sequences alone
+        // fill the device only what is eight times their mean is cut, which cuts at
+        // random hardly ever leave (5003 tokens in 24 sequences of 6 heads 26 -> 20 us,
+        // 20000 in 20 of 16 heads 175 -> 122).
+        const int64_t groups = int64_t(H) * sh.subs;
         len = int64_t(T) * groups / cus;
+        if (groups * num_seqs >= cus) len = std::max(len, 8 * int64_t(T) / num_seqs);
+        len = std::max((len + chunk - 1) / chunk * chunk, (sh.bf16 ? 4 : 2) * chunk);
     } else {
-        const int64_t fit = cus / groups;
-        if (fit < 2) return p;
-        len = (T + fit - 1) / fit;
+        const int64_t groups = int64_t(B) * H;
+        double best = linear_cost(groups, chunks, 1, sh, cus);
+        for (int64_t P = 2; P <= std::min(chunks, kMost); ++P) {
+            const double cost = linear_cost(groups, chunks, P, sh, cus);
+            if (cost < best) best = cost, len = (chunks + P - 1) / P * chunk;
+        }
     }
-    len = std::max((len + gdn2::kLinearChunk - 1) / gdn2::kLinearChunk * gdn2::kLinearChunk, kShortest);
     if (len >= T) return p;
     p.seg_len = int32_t(len);
     p.segments = int32_t((T + len - 1) / len);
@@ -665,13 +693,16 @@ bool linear_sizes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32
 
 LinearPlan linear_fwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, gdn2_dtype dtype)
 {
-    return linear_plan(B, T, H, dk, dv, num_seqs, linear_slices(dv, dk, dtype == GDN2_DTYPE_BF16), device_cus());
+    const bool bf16 = dtype == GDN2_DTYPE_BF16;
+    const int32_t v = linear_slices(dv, dk, bf16);
+    return linear_plan(B, T, H, dk, dv, num_seqs, {v, v, std::max(dk, dv), bf16}, device_cus());
 }
 
 LinearPlan linear_bwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, gdn2_dtype dtype)
 {
     const bool bf16 = dtype == GDN2_DTYPE_BF16;
-    return linear_plan(B, T, H, dk, dv, num_seqs, 2 * linear_slices(dk, dv, bf16) + linear_slices(dv, dk, bf16), device_cus());
+    const int32_t k = linear_slices(dk, dv, bf16), v = linear_slices(dv, dk, bf16);
+    return linear_plan(B, T, H, dk, dv, num_seqs, {2 * k + v, 2 * v, std::max(dk, dv), bf16}, device_cus());
 }
 
 gdn2::LinearLaunch linear_launch(const float* alpha, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t N,

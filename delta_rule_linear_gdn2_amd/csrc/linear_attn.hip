@@ -390,6 +390,23 @@ __device__ __forceinline__ void zero_padding(const LinearLaunch& a, int elem, in
     }
 }
 
+// Four rows of a column of a carry in memory, `p` at the first: rows `sd` apart.
+// Where rows are neighbours (the squares that dq and dk read turned over) they are
+// one access.
+__device__ __forceinline__ f32x4 load_rows4(const float* p, int64_t sd)
+{
+    if (sd == 1) return *reinterpret_cast<const f32x4*>(p);
+    return f32x4{p[0], p[sd], p[2 * sd], p[3 * sd]};
+}
+__device__ __forceinline__ void store_rows4(float* p, int64_t sd, const f32x4& v)
+{
+    if (sd == 1) {
+        *reinterpret_cast<f32x4*>(p) = v;
+        return;
+    }
+    p[0] = v[0], p[sd] = v[1], p[2 * sd] = v[2], p[3 * sd] = v[3];
+}
+
 // What every wavefront of a workgroup knows of its walk.
 struct Place {
     LinearWalk w;
@@ -499,13 +516,11 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
                                   : pl.w.carry_in + (int64_t(pl.n) * a.H + pl.hd) * square + c;
             float* const keep = OUT ? nullptr : pl.w.segment_carry + ((pl.slot + pl.segments - 1) * a.H + pl.hd) * square + c;
 #pragma unroll
-            for (int t = 0; t < TS; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t at = (16 * t + 4 * g + r) * sd;
-                    X[t][r] = p[at];
-                    if (!OUT) keep[at] = X[t][r];
-                }
+            for (int t = 0; t < TS; ++t) {
+                const int64_t at = (16 * t + 4 * g) * sd;
+                X[t] = load_rows4(p + at, sd);
+                if (!OUT) store_rows4(keep + at, sd, X[t]);
+            }
         }
         if (OUT && pl.m > 0) {
             // two segments' carries on their way at a time (one: 0.85 us a segment; four
@@ -518,12 +533,10 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
                 const float* const p1 = two ? p0 + a.H * square : p0;
                 f32x4 v[2][TS];
 #pragma unroll
-                for (int t = 0; t < TS; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[0][t][r] = p0[(16 * t + 4 * g + r) * sd];
-                        v[1][t][r] = p1[(16 * t + 4 * g + r) * sd];
-                    }
+                for (int t = 0; t < TS; ++t) {
+                    v[0][t] = load_rows4(p0 + (16 * t + 4 * g) * sd, sd);
+                    v[1][t] = load_rows4(p1 + (16 * t + 4 * g) * sd, sd);
+                }
 #pragma unroll
                 for (int t = 0; t < TS; ++t)
 #pragma unroll
@@ -689,9 +702,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
             float* p = out + ((OUT ? int64_t(pl.n) : pl.slot) * a.H + pl.hd) * square +
                        (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
 #pragma unroll
-            for (int t = 0; t < TS; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) p[(16 * t + 4 * g + r) * int64_t(pl.w.state_d)] = X[t][r];
+            for (int t = 0; t < TS; ++t) store_rows4(p + (16 * t + 4 * g) * int64_t(pl.w.state_d), pl.w.state_d, X[t]);
         }
     }
 }
