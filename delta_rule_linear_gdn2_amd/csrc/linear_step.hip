@@ -2,11 +2,16 @@
 // (sequence, head), S <- a S + k v^T in place and o = S^T q from the new state.
 //
 // Column j of the state evolves with v_j alone, so one wavefront owns 32
-// columns of a head, as in recurrent_step.hip: lane l holds columns
-// 4 (l & 7) .. + 3 of the dk / 8 rows g dk / 8 .., g = l >> 3.  A lane needs q and k
-// of its own rows only, which it loads for itself (eight lanes the same
-// addresses); the sums over the rows are register sums and three lane exchanges.
-// No LDS and no barrier.
+// columns of a head: lane l holds columns 4 (l & 7) .. + 3 of the rows 8 i + g,
+// g = l >> 3, so that one access takes eight neighbouring rows.  A lane needs q and
+// k of its own rows only, which it loads for itself (eight lanes the same address);
+// the sums over the rows are register sums and three lane exchanges.  No LDS and no
+// barrier.
+//
+// What bounds it is HBM: 256 sequences x 16 heads of 128 x 128 (541 MB) take 101 us,
+// 5.35 TB/s, where a large device copy reaches 5.06.  Rows g dk / 8 .. in each lane
+// took 104 us, all stores behind the last load 106, stores without the system-scope
+// hint 106, plain accesses 109.
 #include "gdn2_device.hpp"
 #include "launch.hpp"
 
@@ -25,25 +30,16 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, int(bytes), 0x00020000);
 }
 
-// N consecutive elements at a boundary of N elements.
-template <int N>
-__device__ __forceinline__ void load_row(const float* p, float (&v)[N])
+__device__ __forceinline__ void load4(const float* p, float (&v)[4])
 {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + i);
-        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-    }
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
 }
-template <int N>
-__device__ __forceinline__ void load_row(const bf16raw* p, float (&v)[N])
+__device__ __forceinline__ void load4(const bf16raw* p, float (&v)[4])
 {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p + i);
-        v[i] = __uint_as_float(x.x << 16), v[i + 1] = __uint_as_float(x.x & 0xffff0000u);
-        v[i + 2] = __uint_as_float(x.y << 16), v[i + 3] = __uint_as_float(x.y & 0xffff0000u);
-    }
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
 }
 __device__ __forceinline__ void store_o4(float* o, const float (&x)[4]) { *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]); }
 __device__ __forceinline__ void store_o4(bf16raw* o, const float (&x)[4])
@@ -72,13 +68,15 @@ __global__ __launch_bounds__(64) void linear_step_kernel(LinearStepArgs a)
 
     const rsrc_t rs = make_rsrc(a.state + head * DK * DV, DK * DV * 4);
     float k[NP], q[NP], v[4];
-    load_row(static_cast<const T*>(a.k) + head * DK + g * NP, k);
-    load_row(static_cast<const T*>(a.v) + head * DV + c0, v);
-    load_row(static_cast<const T*>(a.q) + head * DK + g * NP, q);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) k[i] = load_as_f32(static_cast<const T*>(a.k), head * DK + 8 * i + g);
+    load4(static_cast<const T*>(a.v) + head * DV + c0, v);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) q[i] = load_as_f32(static_cast<const T*>(a.q), head * DK + 8 * i + g);
     const float decay = fminf(fmaxf(a.alpha[head % a.H], 0x1p-15f), 1.0f);
     u32x4 st[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) st[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, ((g * NP + i) * DV + c0) * 4, 0, kAuxLoad);
+    for (int i = 0; i < NP; ++i) st[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, ((8 * i + g) * DV + c0) * 4, 0, kAuxLoad);
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -89,7 +87,7 @@ __global__ __launch_bounds__(64) void linear_step_kernel(LinearStepArgs a)
             y[j] = __float_as_uint(s);
             o[j] += s * q[i];
         }
-        __builtin_amdgcn_raw_buffer_store_b128(y, rs, ((g * NP + i) * DV + c0) * 4, 0, kAuxStore);
+        __builtin_amdgcn_raw_buffer_store_b128(y, rs, ((8 * i + g) * DV + c0) * 4, 0, kAuxStore);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = rowgroup_sum(o[j]);
