@@ -315,8 +315,11 @@ __device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, in
 template <typename T, int DA, int CW, bool OUT>
 struct Shape {
     static constexpr int kOutWaves = OUT ? 4 : 0;  // 16 tokens of a chunk each
-    static constexpr int kStateWaves = CW / 16;  // 16 columns of X each
-    static constexpr int kTiles = DA / 16;       // in tiles of 16 x 16
+    // State wavefronts: 16 columns of X each, in tiles of 16 x 16; half of the rows
+    // where there are no output wavefronts beside them.
+    static constexpr int kStateRows = !OUT && DA >= 64 ? DA / 2 : DA;
+    static constexpr int kStateWaves = CW / 16 * (DA / kStateRows);
+    static constexpr int kTiles = kStateRows / 16;
     static constexpr int kThreads = 64 * (kOutWaves + kStateWaves);
     static constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     static constexpr int PL = kPlanes<T>;
@@ -471,9 +474,10 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     for (int i = tid; i <= kC; i += NT) pw[i] = small_power(al, i);
     lds_barrier();  // pw
 
-    // State wavefronts: columns 16 cb .., this lane column 16 cb + l and rows
-    // 16 t + 4 g + r of tile t.
-    const int cb = STATER ? wave - SH::kOutWaves : 0;
+    // State wavefronts: columns 16 cb .. and rows d0 .., this lane column 16 cb + l
+    // and rows d0 + 16 t + 4 g + r of tile t.
+    const int cb = STATER ? (wave - SH::kOutWaves) % (CW / 16) : 0;
+    const int d0 = STATER ? (wave - SH::kOutWaves) / (CW / 16) * SH::kStateRows : 0;
 
     // Constants of the head: output wavefronts hold the decays of their tiles of P
     // (by the distance of the tile's tokens) and of the carry's read, state
@@ -505,26 +509,25 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) X[t][r] = 0.f;
-        const int64_t sd = pl.w.state_d, square = int64_t(DA) * a.width;
+        const int64_t square = int64_t(DA) * a.width, sd = pl.w.state_d;
         const int64_t c = (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
         if (pl.w.carry_in && pl.m == 0) {
             // Where there are several segments, the launch for carries leaves what comes in
             // in the slot of the last one, which has no carry to keep: the last segment may
             // write the final carry over it while the first still has to read it.
+            float* const keep = pl.w.segment_carry + ((pl.slot + pl.segments - 1) * a.H + pl.hd) * square + c;
+            const float* const in = pl.w.carry_in + (int64_t(pl.n) * a.H + pl.hd) * square + c;
             const bool kept = OUT && pl.segments > 1;
-            const float* p = kept ? pl.w.segment_carry + ((pl.slot + pl.segments - 1) * a.H + pl.hd) * square + c
-                                  : pl.w.carry_in + (int64_t(pl.n) * a.H + pl.hd) * square + c;
-            float* const keep = OUT ? nullptr : pl.w.segment_carry + ((pl.slot + pl.segments - 1) * a.H + pl.hd) * square + c;
 #pragma unroll
             for (int t = 0; t < TS; ++t) {
-                const int64_t at = (16 * t + 4 * g) * sd;
-                X[t] = load_rows4(p + at, sd);
-                if (!OUT) store_rows4(keep + at, sd, X[t]);
+                const int64_t d = d0 + 16 * t + 4 * g;
+                X[t] = load_rows4((kept ? keep : in) + d * sd, sd);
+                if (!OUT) store_rows4(keep + d * sd, sd, X[t]);
             }
         }
         if (OUT && pl.m > 0) {
-            // two segments' carries on their way at a time (one: 0.85 us a segment; four
-            // spill); behind the last one it is read again and has no weight
+            // two segments' carries on their way at a time; behind the last one it is
+            // read again and has no weight
             const float over = power(al, uint32_t(a.seg_len));
             const float* const p = pl.w.segment_carry + ((pl.slot - pl.m) * a.H + pl.hd) * square + c;
             for (int j = 0; j < pl.m; j += 2) {
@@ -646,7 +649,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         for (int s = 0; s < kSteps; ++s) {
             const Scaled<T, EXACT> z(F::template cols<CW>(buf + SH::kOffZ, 16 * cb, s, lane), scale + s * kPer);
 #pragma unroll
-            for (int t = 0; t < TS; ++t) X[t] = z.times(F::template cols<DA>(buf + SH::kOffY, 16 * t, s, lane), X[t]);
+            for (int t = 0; t < TS; ++t) X[t] = z.times(F::template cols<DA>(buf + SH::kOffY, d0 + 16 * t, s, lane), X[t]);
         }
     };
 
@@ -699,10 +702,11 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         float* const out = OUT ? (pl.last ? pl.w.carry_out : nullptr) : pl.w.segment_carry;
         if (out) {
             const int64_t square = int64_t(DA) * a.width;
-            float* p = out + ((OUT ? int64_t(pl.n) : pl.slot) * a.H + pl.hd) * square +
-                       (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
+            const int64_t sd = pl.w.state_d;
+            float* const p = out + ((OUT ? int64_t(pl.n) : pl.slot) * a.H + pl.hd) * square +
+                             (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
 #pragma unroll
-            for (int t = 0; t < TS; ++t) store_rows4(p + (16 * t + 4 * g) * int64_t(pl.w.state_d), pl.w.state_d, X[t]);
+            for (int t = 0; t < TS; ++t) store_rows4(p + (d0 + 16 * t + 4 * g) * sd, sd, X[t]);
         }
     }
 }
