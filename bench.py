@@ -482,6 +482,48 @@ def bench_training(args):
     return rows
 
 
+def bench_linear(args):
+    """Linear attention with a fixed decay for each head, and the norms and
+    rotation of its queries and keys, on batched_bf16's and decode_b256's shapes:
+    one report row each."""
+    import torch
+
+    from delta_rule_linear_gdn2_amd import binding
+
+    B, T, H, d, N = 8, 4096, 16, 128, 256
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def new(*shape, scale=1.0):
+        return (scale * torch.randn(shape, generator=gen, device="cuda")).to(torch.bfloat16)
+
+    q, k, v, d_o = new(B, T, H, d, scale=d ** -0.5), new(B, T, H, d), new(B, T, H, d), new(B, T, H, d)
+    alpha = torch.exp(-(2.0 ** (-8.0 * (torch.arange(H, device="cuda") + 1) / H)))
+    freq = 1e4 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float32) / d)
+    w = torch.ones(d, dtype=torch.float32, device="cuda")
+    token = [new(N, H, d) for _ in range(3)]
+    state = 0.1 * torch.randn((N, H, d, d), generator=gen, device="cuda")
+    how = dict(inv_freq=freq, weight_q=w, weight_k=w, q_scale=d ** -0.5)
+    n = 2 * B * T * H * d  # bytes of one [B, T, H, d] tensor
+    calls = (("batched_bf16 linear attention (gdn2_linear_attn_fwd)", 4 * n,
+              lambda: binding.gdn2_linear_attn_fwd(q, k, v, alpha, output_final_state=False)),
+             ("batched_bf16 linear attention backward", 7 * n, lambda: binding.gdn2_linear_attn_bwd(q, k, v, alpha, d_o)),
+             ("decode_b256 linear attention step", 8 * N * H * d * d + 8 * N * H * d,
+              lambda: binding.gdn2_linear_attn_step(*token, alpha, state)),
+             ("batched_bf16 q, k norm and rotation (gdn2_qk_norm_rope)", 4 * n,
+              lambda: binding.gdn2_qk_norm_rope(q, k, **how)),
+             ("batched_bf16 q, k norm and rotation backward", 6 * n,
+              lambda: binding.gdn2_qk_norm_rope_bwd(q, k, v, d_o, **how)))
+    rows = []
+    for name, nbytes, call in calls:
+        per, _, _ = time_events(call, args.warmup, args.steps)
+        ms = float(np.median(per))
+        log(f"{name}: {ms * 1e3:.1f} us, {nbytes / (ms / 1e3) / 1e9:.0f} GB/s")
+        rows.append({"report": "config", "workload": name, "us_per_call": ms * 1e3,
+                     "GBps": nbytes / (ms / 1e3) / 1e9, "hbm_frac": nbytes / (ms / 1e3) / 1e9 / HBM_PEAK_GBPS,
+                     "algorithmic_bytes": nbytes})
+    return rows
+
+
 def run_only(args):
     """One part alone (for rocprofv3 runs); prints one JSON line."""
     import torch
@@ -506,6 +548,8 @@ def run_only(args):
         res = {"part": "mixer", "rows": bench_mixer(args), "launches": args.steps + args.warmup}
     elif args.only == "training":
         res = {"part": "training", "rows": bench_training(args), "launches": args.steps + args.warmup}
+    elif args.only == "linear":
+        res = {"part": "linear", "rows": bench_linear(args), "launches": args.steps + args.warmup}
     else:
         nbytes = 1 << 30
         src = torch.empty(nbytes // 4, dtype=torch.float32, device="cuda").fill_(1.0)
@@ -634,6 +678,9 @@ def run_configs(args):
     # the training operators around it
     for row in bench_training(args):
         print(json.dumps(row), flush=True)
+    # linear attention with a fixed decay, and the queries and keys that it reads
+    for row in bench_linear(args):
+        print(json.dumps(row), flush=True)
     # the gate-aware backward on the headline shape, and the oracle's reverse mode beside it
     bw = bench_bwd(args)
     t0 = time.perf_counter()
@@ -694,7 +741,7 @@ def main():
                     help="untimed chunkwise launches before the warm-up ones, so that the timed launches run on a "
                          "settled shader clock (headline line and --configs; --only parts take none)")
     ap.add_argument("--no-decode", action="store_true", help="skip the decode half")
-    ap.add_argument("--only", choices=["chunk", "decode", "copy", "bwd", "mixer", "training", "segmented"], default=None,
+    ap.add_argument("--only", choices=["chunk", "decode", "copy", "bwd", "mixer", "training", "linear", "segmented"], default=None,
                     help="profiling aid: run one part only and print its timing line "
                          "(copy = a plain 1 GiB device copy, the reference for HBM byte counters; "
                          "segmented = layer_bf16 through the few-chain segmented path)")

@@ -885,14 +885,18 @@ def _four(name, t):
     return t.shape
 
 
-@functools.lru_cache(maxsize=256)
 def gdn2_linear_attn_fwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code) -> int:
     return int(load().gdn2_linear_attn_fwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code))
 
 
-@functools.lru_cache(maxsize=256)
 def gdn2_linear_attn_bwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code) -> int:
     return int(load().gdn2_linear_attn_bwd_workspace_bytes(B, T, H, dk, dv, num_seqs, dtype_code))
+
+
+@functools.lru_cache(maxsize=512)
+def _linear_workspace(name, device, *sizes):
+    """The query's answer on a device: the plan goes by its compute units."""
+    return int(getattr(_LIB, name)(*sizes))
 
 
 @_on_stream
@@ -931,7 +935,7 @@ def gdn2_linear_attn_fwd(q, k, v, alpha, initial_state=None, *, output_final_sta
     elif output_final_state:
         final_state = alpha.new_empty(st_shape)
     packed = N if cu_seqlens is not None else 0
-    need = gdn2_linear_attn_fwd_workspace_bytes(B, T, H, dk, dv, packed, code) if segmented else 0
+    need = _linear_workspace("gdn2_linear_attn_fwd_workspace_bytes", index, B, T, H, dk, dv, packed, code) if segmented else 0
     workspace, ws_bytes = _workspace(workspace, need, q)
     _run("gdn2_linear_attn_fwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), _addr(initial_state),
          _addr(final_state), out.data_ptr(), _addr(cu_seqlens), B, T, H, dk, dv, packed, new, code, _addr(workspace),
@@ -968,7 +972,7 @@ def gdn2_linear_attn_bwd(q, k, v, alpha, d_o, *, initial_state=None, d_final_sta
     out = {"dq": new(q), "dk": new(k), "dv": new(v),
            "d_initial_state": alpha.new_empty(st_shape) if output_d_initial_state else None}
     packed = N if cu_seqlens is not None else 0
-    need = gdn2_linear_attn_bwd_workspace_bytes(B, T, H, dk, dv, packed, code) if segmented else 0
+    need = _linear_workspace("gdn2_linear_attn_bwd_workspace_bytes", index, B, T, H, dk, dv, packed, code) if segmented else 0
     workspace, ws_bytes = _workspace(workspace, need, q)
     _run("gdn2_linear_attn_bwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), _addr(initial_state),
          d_o.data_ptr(), _addr(d_final_state), *[_addr(t) for t in out.values()], _addr(cu_seqlens), B, T, H, dk, dv,

@@ -29,12 +29,22 @@
 // operands take the same (see Frag).  The decays of a tile are constants of the
 // head: each lane keeps its own in registers for the whole walk.
 //
-// Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  P and the
-// copy of X that the outputs read are rounded to bf16, as the outputs are: each
-// adds to an output what its own rounding does.  X itself is FP32.  Where the
-// caller gets it, the factor a^n z of its update goes in as three bf16 terms that
-// hold all 24 bits, so that it is the state of FP32 arithmetic; where only the
-// bf16 copy is read, as two (2^-17).
+// Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  P goes into its
+// product as two bf16 terms (2^-17); the copy of X that the outputs read is rounded
+// to bf16, which adds to an output, over the dk terms of its sum, what its own
+// rounding does.  X itself is FP32.  Where the caller gets it, the factor a^n z of
+// its update goes in as three bf16 terms that hold all 24 bits, so that it is the
+// state of FP32 arithmetic; where only the bf16 copy is read, as two.  FP32 inputs
+// are three bf16 terms throughout.
+//
+// What bounds it (8 sequences x 4096 tokens x 16 heads of 128, bf16; 64 chunks a
+// workgroup, one workgroup a compute unit): 121 us, where its 537 MB take 106 at a
+// large copy's rate.  Without products the same loads, staging and stores take 112,
+// without loads the products 88.  A chunk's turn takes about 1100 cycles of matrix
+// instructions and 1100 of vector ones on each SIMD; on the two wavefronts that it
+// has they overlap in part.  Two workgroups a compute unit (128 registers a lane)
+// spill loads in flight: 177 to 296 us.  Tiles of 32 x 32 with each tile of P formed
+// twice: 143.  Loads two chunks ahead instead of one: the same.
 #include "gdn2_device.hpp"
 #include "launch.hpp"
 
@@ -292,21 +302,26 @@ __device__ __forceinline__ float small_power(float alpha, int n)
 // Segment m of sequence n in [0, slots): slot = start / seg_len + n + m, which
 // is distinct for distinct segments of offsets that do not decrease, and below
 // T / seg_len + N for any.  Finds n: the last sequence whose first slot is not
-// above `slot`.
+// above `slot`, 64 sequences or borders of 64 ranges at a time.
 __device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, int seg_len, int slot, int lane)
 {
-    int n = 0;
-    for (int base = 0; base < N; base += 64) {
-        const int i = base + lane;
-        int at = 0x7fffffff;
-        if (i < N) {
+    int lo = 0, count = N;
+    while (true) {
+        const int step = (count + 63) / 64, i = lo + lane * step;
+        bool below = false;
+        if (lane * step < count) {
             int b = cu[i];
             b = b < 0 ? 0 : b > T ? T : b;
-            at = b / seg_len + i;
+            below = b / seg_len + i <= slot;
         }
-        n += __popcll(__ballot(at <= slot));
+        const int n = __popcll(__ballot(below));
+        if (n > 0) {
+            lo += (n - 1) * step;
+            count -= (n - 1) * step;
+        }
+        if (step == 1) return lo;
+        count = count < step ? count : step;
     }
-    return n > 0 ? n - 1 : 0;
 }
 
 // A workgroup's wavefronts and LDS.  bf16 keeps two chunks in LDS, so that one is
@@ -608,13 +623,31 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
                 for (int r = 0; r < 4; ++r) o[k - NP][r] = acc[r] * read;
             }
         }
-        F pf[NJ];
+        // bf16: P goes in as two terms.  Rounded to one, a lone token's outputs would all
+        // be off by the rounding of its q . k (3% of the forward at the training shape).
+        constexpr int kTerms = SH::PL == 1 ? 2 : 1;
+        F pf[NJ][kTerms];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) pf[j] = F::from_acc(p + 2 * j);
+        for (int j = 0; j < NJ; ++j) {
+            if constexpr (kTerms == 1) {
+                pf[j][0] = F::from_acc(p + 2 * j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t t[2];
+                    split_pair<2>(p[2 * j + (i >> 1)][2 * (i & 1)], p[2 * j + (i >> 1)][2 * (i & 1) + 1], t);
+                    const uint32_t hi[1] = {t[0]}, lo[1] = {t[1]};
+                    pf[j][0].put(i, hi);
+                    pf[j][1].put(i, lo);
+                }
+            }
+        }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) o[c] = zf[c * NJ + j].times(pf[j], o[c]);
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int k = kTerms - 1; k >= 0; --k) o[c] = zf[c * NJ + j].times(pf[j][k], o[c]);
             const int col = 16 * c + 4 * g, per = 16 / EB;
             put4(lO + Tile<T, CW>::off(16 * ROLE + l, col / per) + (col % per) * EB, o[c], static_cast<T*>(nullptr));
         }

@@ -578,10 +578,12 @@ size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, 
  * 2^15, B T H and num_seqs H at most 2^40.  Outputs and the workspace must not
  * overlap inputs (but final_state = initial_state) or each other.
  *
- * bf16 inputs feed bf16 products with FP32 sums; the states are those of FP32
- * arithmetic, and their copy that o reads is rounded to bf16.  Inside a 64-token
- * chunk of a sequence a NaN or infinity in v or k reaches the outputs of the
- * chunk's earlier tokens too (they multiply it by zero).
+ * bf16 inputs feed bf16 products with FP32 sums; states that a call returns are
+ * those of FP32 arithmetic, the copy of a state that o reads is rounded to bf16.
+ * FP32 inputs are split into three bf16 terms (products off by 2^-24; entries below
+ * 1e-33 keep fewer bits).  A NaN or infinity in k or v of a token gives NaN in its
+ * head's later outputs and state, and in the outputs of the earlier tokens of its
+ * 64-token chunk (they multiply it by zero); other heads and sequences keep theirs.
  */
 gdn2_status gdn2_linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha,
                                  const float* initial_state, float* final_state, void* o, const int32_t* cu_seqlens,
