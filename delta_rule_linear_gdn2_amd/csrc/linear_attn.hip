@@ -21,7 +21,7 @@
 //
 // Work split.  One workgroup walks one (sequence segment, head, slice of up to
 // 64 columns of z).  X's slice stays in the matrix accumulators of its state
-// wavefronts; the output wavefronts (32 tokens x 32 columns each) form
+// wavefronts, 16 columns each; four output wavefronts, 16 tokens of a chunk each, form
 //     P^T = Y X^T (tokens j x i), masked and decayed in registers, then
 //     O^T = Xs^T X^T + Z^T P^T  (columns x tokens i),
 // where an accumulator tile is directly the next product's operand, because a
@@ -43,7 +43,8 @@
 // without loads the products 88.  A chunk's turn takes about 1100 cycles of matrix
 // instructions and 1100 of vector ones on each SIMD; on the two wavefronts that it
 // has they overlap in part.  Two workgroups a compute unit (128 registers a lane)
-// spill loads in flight: 177 to 296 us.  Tiles of 32 x 32 with each tile of P formed
+// spill loads in flight: 177 to 296 us; twelve wavefronts, with the state's rows halved
+// here too, take 127.  Tiles of 32 x 32 with each tile of P formed
 // twice: 143.  Loads two chunks ahead instead of one: the same.
 #include "gdn2_device.hpp"
 #include "launch.hpp"
@@ -490,7 +491,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     lds_barrier();  // pw
 
     // State wavefronts: columns 16 cb .. and rows d0 .., this lane column 16 cb + l
-    // and rows d0 + 16 t + 4 g + r of tile t.
+    // and rows d0 + 16 t + 4 g + r of tile t (d0 = 0 where OUT).
     const int cb = STATER ? (wave - SH::kOutWaves) % (CW / 16) : 0;
     const int d0 = STATER ? (wave - SH::kOutWaves) / (CW / 16) * SH::kStateRows : 0;
 

@@ -23,6 +23,11 @@
 // rot / 2 + 4 l ..; neighbours and channels behind rot: 8 l ..).  A wavefront takes
 // 512 / d heads of a token at a time.  Its lane groups share the sines: group g
 // forms pair g & 3 of each lane, and four lane exchanges hand them round.
+//
+// What bounds it: memory.  8 x 4096 tokens of 16 + 16 heads of 128, bf16: 99 us for
+// 537 MB (5.4 TB/s; a 1 GiB copy reaches 5.1), vector arithmetic in 46% of the
+// cycles; backwards 151 us for 805 MB, of which the sum of the weights' gradients
+// takes 5.  Calls of a few tokens take 5 us on the device, less than their host time.
 #include "row_device.hpp"
 
 namespace gdn2 {
@@ -245,8 +250,9 @@ __global__ __launch_bounds__(kThreads) void qk_rope_bwd_kernel(QkRopeBwdArgs a)
 }
 
 // Workgroups: as many as are resident at once (four wavefronts a SIMD), fewer
-// for small calls; a token's heads are shared out where the tokens alone do not
-// fill the device.
+// for small calls (twice as many: 104 and 161 us instead of 99 and 151); a token's
+// heads are shared out where the tokens alone do not fill the device (shares half or
+// a quarter of these: the same).
 constexpr int64_t kFull = 1024;
 
 int rope_parts(int64_t tokens, int heads_q, int heads_k, int d)
