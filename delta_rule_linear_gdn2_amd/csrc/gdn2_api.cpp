@@ -627,10 +627,11 @@ struct LinearPlan {
 
 int32_t linear_slices(int32_t width, int32_t da, bool bf16) { return width / gdn2::linear_slice(width, da, bf16); }
 
-// What the plan needs to know of a call: its workgroups per (sequence, head), in the
-// launch for outputs and in the one for carries.
+// What the plan needs to know of a call: its workgroups per (sequence, head), in all
+// launches for outputs, in the largest of them (a backward with dk != dv has two, one
+// behind the other) and in the one for carries.
 struct LinearShape {
-    int32_t subs, carry_subs, widest;
+    int32_t all_subs, subs, carry_subs, widest;
     bool bf16;
 };
 
@@ -640,6 +641,8 @@ struct LinearShape {
 // segment's carry 0.5, the launch for carries 7 and half a walk's slots.  In one
 // piece / by this rule: 4096 tokens of 16 heads of 128 forward 102 / 42, 1024 tokens
 // 29 / 21, 16384 tokens of 2 heads 390 / 57; 512 tokens 17.1 / in two chunks 17.8.
+// Backward, FP32, 4096 tokens of 4 heads of 64 x 128: 71; counting the workgroups of
+// its two launches as one's, 91.
 double linear_cost(int64_t groups, int64_t chunks, int64_t P, const LinearShape& sh, int64_t cus)
 {
     const double chunk = sh.bf16 ? (sh.widest < 128 ? 1.0 : 1.5) : (sh.widest < 128 ? 2.4 : 4.5);
@@ -660,13 +663,16 @@ LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, 
     p.slots = rows;
     int64_t len = T;
     if (num_seqs > 0) {
-        // The lengths are on the device.  Segments of a compute unit's share of the
-        // whole, none under four chunks (FP32: two); but where the sequences alone
+        // The lengths are on the device.  Segments of 0.8 of a compute unit's share of
+        // the whole (sequences end inside segments, and a round of fewer chunks more is
+        // better than one more chunk: FP32 backward of 3001 tokens in 7 sequences of 4
+        // heads of 64 x 128 67 -> 57 us, 12000 bf16 in 6 of 8 101 -> 94; at 0.6 64 and
+        // 112), none under four chunks (FP32: two); but where the sequences alone
         // fill the device only what is eight times their mean is cut, which cuts at
         // random hardly ever leave (5003 tokens in 24 sequences of 6 heads 26 -> 20 us,
         // 20000 in 20 of 16 heads 175 -> 122).
-        const int64_t groups = int64_t(H) * sh.subs;
-        len = int64_t(T) * groups / cus;
+        const int64_t groups = int64_t(H) * sh.all_subs;
+        len = int64_t(T) * groups * 4 / (5 * int64_t(cus));
         if (groups * num_seqs >= cus) len = std::max(len, 8 * int64_t(T) / num_seqs);
         len = std::max((len + chunk - 1) / chunk * chunk, (sh.bf16 ? 4 : 2) * chunk);
     } else {
@@ -695,14 +701,15 @@ LinearPlan linear_fwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t 
 {
     const bool bf16 = dtype == GDN2_DTYPE_BF16;
     const int32_t v = linear_slices(dv, dk, bf16);
-    return linear_plan(B, T, H, dk, dv, num_seqs, {v, v, std::max(dk, dv), bf16}, device_cus());
+    return linear_plan(B, T, H, dk, dv, num_seqs, {v, v, v, std::max(dk, dv), bf16}, device_cus());
 }
 
 LinearPlan linear_bwd_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs, gdn2_dtype dtype)
 {
     const bool bf16 = dtype == GDN2_DTYPE_BF16;
     const int32_t k = linear_slices(dk, dv, bf16), v = linear_slices(dv, dk, bf16);
-    return linear_plan(B, T, H, dk, dv, num_seqs, {2 * k + v, 2 * v, std::max(dk, dv), bf16}, device_cus());
+    const int32_t all = 2 * k + v, most = dk == dv ? all : std::max(2 * k, v);
+    return linear_plan(B, T, H, dk, dv, num_seqs, {all, most, 2 * v, std::max(dk, dv), bf16}, device_cus());
 }
 
 gdn2::LinearLaunch linear_launch(const float* alpha, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t H, int32_t N,
