@@ -30,7 +30,7 @@
 // head: each lane keeps its own in registers for the whole walk.
 //
 // Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  P goes into its
-// product as two bf16 terms (2^-17); the copy of X that the outputs read is rounded
+// product as two bf16 terms (2^-16); the copy of X that the outputs read is rounded
 // to bf16, which adds to an output, over the dk terms of its sum, what its own
 // rounding does.  X itself is FP32.  Where the caller gets it, the factor a^n z of
 // its update goes in as three bf16 terms that hold all 24 bits, so that it is the
@@ -105,17 +105,28 @@ struct Tile {
     static __device__ __forceinline__ int off(int row, int granule) { return row * kRow + ((granule ^ swz(row)) << 4); }
 };
 
-// FP32 values as the sum of three bf16 ones, each the upper 16 bits of what the
-// ones before leave: together all 24 bits.  (An infinity leaves a NaN behind it.)
+// FP32 values as the sum of N bf16 ones, each of what the ones before leave.  Three
+// hold all 24 bits; their leading terms are rounded to nearest, so that what they
+// leave is at most 2^-8 and 2^-17 of the value and of either sign (cut off, it is
+// twice that with the value's own sign, which shrinks every product of two values by
+// up to 2^-21; rounding costs 2% of the FP32 calls).  Of two, the first is cut off and
+// the second rounded: off by 2^-16, of either sign.  (An infinity leaves a NaN
+// behind it, and three terms take what rounds to one, from 2^128 (1 - 2^-9), for one.)
 template <int N>
 __device__ __forceinline__ void split_pair(float lo, float hi, uint32_t (&t)[N])
 {
 #pragma unroll
     for (int k = 0; k < N - 1; ++k) {
-        const uint32_t ul = __float_as_uint(lo), uh = __float_as_uint(hi);
-        t[k] = __builtin_amdgcn_perm(uh, ul, 0x07060302);  // the upper halves
-        lo -= __uint_as_float(ul & 0xffff0000u);
-        hi -= __uint_as_float(uh & 0xffff0000u);
+        if constexpr (N == 3) {
+            t[k] = pack2(lo, hi);
+            lo -= __uint_as_float(t[k] << 16);
+            hi -= __uint_as_float(t[k] & 0xffff0000u);
+        } else {
+            const uint32_t ul = __float_as_uint(lo), uh = __float_as_uint(hi);
+            t[k] = __builtin_amdgcn_perm(uh, ul, 0x07060302);  // the upper halves
+            lo -= __uint_as_float(ul & 0xffff0000u);
+            hi -= __uint_as_float(uh & 0xffff0000u);
+        }
     }
     t[N - 1] = pack2(lo, hi);
 }
@@ -132,8 +143,8 @@ constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
 //             every 16 rows the four 4 g .. + 3 that a lane holds in a 16 x 16
 //             accumulator, so that
 //   from_acc: two accumulator tiles are the other operand as they are.
-// FP32 operands are three bf16 planes, and a product six: what is left out is
-// 2^-24 of it.  (The FP32 matrix instructions take 2.7 times as long.)
+// FP32 operands are three bf16 planes, and a product six: what is left out, the
+// second plane times the third and below, is at most 2^-24 of it.  (The FP32 matrix instructions take 2.7 times as long.)
 template <typename T>
 struct Frag {
     static constexpr int PL = kPlanes<T>;

@@ -581,7 +581,7 @@ size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, 
  * bf16 inputs feed bf16 products with FP32 sums; states that a call returns are
  * those of FP32 arithmetic, the copy of a state that o reads is rounded to bf16.
  * FP32 inputs are split into three bf16 terms (products off by 2^-24; entries below
- * 1e-33 keep fewer bits).  A NaN or infinity in k or v of a token gives NaN in its
+ * 1e-33 keep fewer bits, and finite ones from 2^128 (1 - 2^-9) count as infinite).  A NaN or infinity in k or v of a token gives NaN in its
  * head's later outputs and state, and in the outputs of the earlier tokens of its
  * 64-token chunk (they multiply it by zero); other heads and sequences keep theirs.
  */
