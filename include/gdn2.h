@@ -581,9 +581,9 @@ size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, 
  * bf16 inputs feed bf16 products with FP32 sums; states that a call returns are
  * those of FP32 arithmetic, the copy of a state that o reads is rounded to bf16.
  * FP32 inputs are split into three bf16 terms (products off by 2^-24; entries below
- * 1e-33 keep fewer bits, and finite ones from 2^128 (1 - 2^-9) count as infinite).  A NaN or infinity in k or v of a token gives NaN in its
- * head's later outputs and state, and in the outputs of the earlier tokens of its
- * 64-token chunk (they multiply it by zero); other heads and sequences keep theirs.
+ * 1e-33 keep fewer bits, and finite ones from 2^128 (1 - 2^-9) count as infinite).  What is not
+ * finite in a token reaches what the recurrence lets it reach, its own and its head's
+ * later outputs and the state, and nothing else; an infinity may arrive as NaN.
  */
 gdn2_status gdn2_linear_attn_fwd(const void* q, const void* k, const void* v, const float* alpha,
                                  const float* initial_state, float* final_state, void* o, const int32_t* cu_seqlens,
@@ -603,7 +603,8 @@ size_t gdn2_linear_attn_fwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int
  *     dq_t = S_t d_o_t                     R_t = q_t d_o_t^T + a R_{t+1}
  *     dk_t = R_t v_t     dv_t = R_t^T k_t  d_initial_state = a R_0
  * (the last token's R adds d_final_state).  Nothing is saved by the forward
- * call.
+ * call.  What is not finite reaches what these formulas let it reach, as in the
+ * forward call.
  *
  *   q .. alpha, initial_state, cu_seqlens and the sizes: the forward call's.
  *   d_o  : [B, T, H, dv] dtype.
