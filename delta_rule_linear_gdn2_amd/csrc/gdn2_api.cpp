@@ -621,8 +621,9 @@ constexpr int32_t kLinearMaxHeads = 1 << 15;  // a chunk's rows stay inside the 
 // time; more than one segment a sequence takes a launch more, for their carries.
 struct LinearPlan {
     int32_t seg_len = 0, segments = 1;
-    int64_t slots = 0;
-    size_t carry_bytes = 0;  // one state per slot and head
+    int64_t slots = 0;       // that the walks for outputs are started for (see linear_attn.hip)
+    int64_t carries = 0;     // that the launch for carries is started for
+    size_t carry_bytes = 0;  // one state per carry and head; packed, one more for what comes in
 };
 
 int32_t linear_slices(int32_t width, int32_t da, bool bf16) { return width / gdn2::linear_slice(width, da, bf16); }
@@ -686,8 +687,9 @@ LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, 
     if (len >= T) return p;
     p.seg_len = int32_t(len);
     p.segments = int32_t((T + len - 1) / len);
-    p.slots = num_seqs > 0 ? T / len + num_seqs : rows * p.segments;
-    p.carry_bytes = align256(size_t(p.slots) * size_t(H) * size_t(dk) * size_t(dv) * 4);
+    p.carries = num_seqs > 0 ? T / len : rows * p.segments;
+    p.slots = num_seqs > 0 ? T / len + num_seqs : p.carries;
+    p.carry_bytes = align256(size_t(num_seqs > 0 ? 2 * p.carries : p.carries) * size_t(H) * size_t(dk) * size_t(dv) * 4);
     return p;
 }
 
@@ -720,7 +722,7 @@ gdn2::LinearLaunch linear_launch(const float* alpha, const int32_t* cu_seqlens, 
     a.cu_seqlens = cu_seqlens;
     a.B = B, a.T = T, a.H = H, a.N = N;
     a.seg_len = p.seg_len, a.segments = p.segments;
-    a.units = p.slots * H;
+    a.units = p.slots * H, a.carry_units = p.carries * H;
     a.pad_blocks = cu_seqlens && zero_padding && T > 0 ? 64 : 0;
     return a;
 }

@@ -260,7 +260,7 @@ struct LinearWalk {
     void* out;
     const float* carry_in;   // [N][H] squares, or null (zeros)
     float* carry_out;        // [N][H] squares, or null
-    float* segment_carry;    // [slots][H] squares: a segment's own carry, or null without segments
+    float* segment_carry;    // squares, by place and head: the segments' own carries, or null without segments
     int32_t state_d, state_c;  // strides of a square's row d (of DA) and column c (of width)
     int32_t back;            // walk from the sequence's end
 };
@@ -271,10 +271,11 @@ struct LinearLaunch {
     const int32_t* cu_seqlens;
     int32_t B, T, H, N, width;
     // Sequences are walked in segments of seg_len tokens: `segments` for each
-    // batch row, or, packed, slots start / seg_len + n + m (segments == 1: one
-    // slot a sequence).  units = slots x H.
+    // batch row, or, packed, as slots and windows say (find_sequence; segments == 1:
+    // one segment a sequence).  Units are H for each segment or slot, and in a launch
+    // for carries only for each segment or window.
     int32_t seg_len, segments;
-    int64_t units;
+    int64_t units, carry_units;
     int64_t walk_blocks;     // set by the launch
     int32_t pad_blocks;      // blocks that write zeros to rows that no sequence owns
 };

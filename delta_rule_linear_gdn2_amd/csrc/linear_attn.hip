@@ -325,11 +325,18 @@ __device__ __forceinline__ float small_power(float alpha, int n)
     return float(p);
 }
 
-// Segment m of sequence n in [0, slots): slot = start / seg_len + n + m, which
-// is distinct for distinct segments of offsets that do not decrease, and below
-// T / seg_len + N for any.  Finds n: the last sequence whose first slot is not
-// above `slot`, 64 sequences or borders of 64 ranges at a time.
-__device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, int seg_len, int slot, int lane)
+// Packed sequences.  Segment m of sequence n has
+//   the slot start / seg_len + n + m, distinct for distinct segments of offsets that
+//   do not decrease, and below T / seg_len + N for any;
+//   the window start / seg_len + m, distinct for distinct segments but the last ones
+//   of their sequences, and for those below T / seg_len: a sequence of s > 1 segments
+//   ends at or behind window start / seg_len + s - 1, where the next one's begin.
+// So a workgroup for every slot finds every segment, and a workgroup and a place for
+// every window every segment whose carry is read.  The first window of a sequence of
+// several segments is also its own alone.
+// Finds n: the last sequence whose first slot (each = 1) or window (each = 0) is not
+// above `at`, 64 sequences or borders of 64 ranges at a time.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int T, int seg_len, int each, int at, int lane)
 {
     int lo = 0, count = N;
     while (true) {
@@ -338,7 +345,7 @@ __device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, in
         if (lane * step < count) {
             int b = cu[i];
             b = b < 0 ? 0 : b > T ? T : b;
-            below = b / seg_len + i <= slot;
+            below = b / seg_len + each * i <= at;
         }
         const int n = __popcll(__ballot(below));
         if (n > 0) {
@@ -455,7 +462,8 @@ __device__ __forceinline__ void store_rows4(float* p, int64_t sd, const f32x4& v
 struct Place {
     LinearWalk w;
     int n, m, segments, hd, col0;  // segment m of sequence n's `segments`
-    int64_t slot, row0, tok;  // tok: forwards the next token, backwards the one behind it
+    int64_t carry, kept;      // where segment 0's carry is, and what comes in while there are several
+    int64_t row0, tok;        // tok: forwards the next token, backwards the one behind it
     int left;                 // tokens to walk
     bool last;                // the sequence's last segment
 };
@@ -553,10 +561,10 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         const int64_t square = int64_t(DA) * a.width, sd = pl.w.state_d;
         const int64_t c = (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
         if (pl.w.carry_in && pl.m == 0) {
-            // Where there are several segments, the launch for carries leaves what comes in
-            // in the slot of the last one, which has no carry to keep: the last segment may
-            // write the final carry over it while the first still has to read it.
-            float* const keep = pl.w.segment_carry + ((pl.slot + pl.segments - 1) * a.H + pl.hd) * square + c;
+            // Where there are several segments, the launch for carries keeps what comes in:
+            // the last segment may write the final carry over it while the first still has
+            // to read it.
+            float* const keep = pl.w.segment_carry + (pl.kept * a.H + pl.hd) * square + c;
             const float* const in = pl.w.carry_in + (int64_t(pl.n) * a.H + pl.hd) * square + c;
             const bool kept = OUT && pl.segments > 1;
 #pragma unroll
@@ -570,7 +578,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
             // two segments' carries on their way at a time; behind the last one it is
             // read again and has no weight
             const float over = power(al, uint32_t(a.seg_len));
-            const float* const p = pl.w.segment_carry + ((pl.slot - pl.m) * a.H + pl.hd) * square + c;
+            const float* const p = pl.w.segment_carry + (pl.carry * a.H + pl.hd) * square + c;
             for (int j = 0; j < pl.m; j += 2) {
                 const bool two = j + 1 < pl.m;
                 const float* const p0 = p + j * a.H * square;
@@ -795,7 +803,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         if (out) {
             const int64_t square = int64_t(DA) * a.width;
             const int64_t sd = pl.w.state_d;
-            float* const p = out + ((OUT ? int64_t(pl.n) : pl.slot) * a.H + pl.hd) * square +
+            float* const p = out + ((OUT ? int64_t(pl.n) : pl.carry + pl.m) * a.H + pl.hd) * square +
                              (pl.col0 + 16 * cb + l) * int64_t(pl.w.state_c);
 #pragma unroll
             for (int t = 0; t < TS; ++t) store_rows4(p + (d0 + 16 * t + 4 * g) * sd, sd, X[t]);
@@ -825,18 +833,20 @@ __global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) __attribute__((a
     pl.w = a.walk[sub / slices];
     pl.col0 = (sub % slices) * CW;
     pl.hd = int(unit % a.H);
-    pl.slot = unit / a.H;
-    pl.n = !a.cu_seqlens       ? int(pl.slot / a.segments)
-           : a.segments == 1 ? int(pl.slot)
-                               : __builtin_amdgcn_readfirstlane(slot_sequence(a.cu_seqlens, a.N, a.T, a.seg_len, int(pl.slot), lane));
+    const int64_t at = unit / a.H;  // a segment (batched), a slot (packed) or a window (packed, carries)
+    pl.n = !a.cu_seqlens       ? int(at / a.segments)
+           : a.segments == 1 ? int(at)
+                               : __builtin_amdgcn_readfirstlane(find_sequence(a.cu_seqlens, a.N, a.T, a.seg_len, OUT, int(at), lane));
     int64_t bos, eos, brow;
     sequence_bounds(a.cu_seqlens, pl.n, a.T, bos, eos, brow);
-    pl.m = a.segments == 1 ? 0 : a.cu_seqlens ? int(pl.slot - (bos / a.seg_len + pl.n)) : int(pl.slot % a.segments);
+    pl.m = a.segments == 1 ? 0 : a.cu_seqlens ? int(at - (bos / a.seg_len + (OUT ? pl.n : 0))) : int(at % a.segments);
     const int64_t len = eos - bos, before = int64_t(pl.m) * a.seg_len;  // tokens walked before this segment
     if (pl.m < 0 || (pl.m > 0 && before >= len)) return;
     pl.segments = len > a.seg_len ? int((len + a.seg_len - 1) / a.seg_len) : 1;
     pl.last = len - before <= a.seg_len;
     if (!OUT && pl.last) return;                                       // no segment needs its carry
+    pl.carry = a.cu_seqlens ? bos / a.seg_len : int64_t(pl.n) * a.segments;
+    pl.kept = a.cu_seqlens ? a.T / a.seg_len + pl.carry : pl.carry + pl.segments - 1;  // batched: the last one's place
     pl.left = int(pl.last ? len - before : a.seg_len);
     pl.row0 = brow * a.T;
     pl.tok = pl.w.back ? eos - before : bos + before;
@@ -854,6 +864,7 @@ __global__ __launch_bounds__((Shape<T, DA, CW, OUT>::kThreads)) __attribute__((a
 template <typename T, int DA, int CW, bool OUT>
 hipError_t launch_shape(LinearLaunch a, bool exact, hipStream_t stream)
 {
+    if (!OUT) a.units = a.carry_units;
     a.walk_blocks = (a.units + 7) / 8 * 8 * (a.width / CW) * a.walks;
     const int64_t blocks = a.walk_blocks + (OUT ? a.pad_blocks : 0);
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;

@@ -592,7 +592,8 @@ gdn2_status gdn2_linear_attn_fwd(const void* q, const void* k, const void* v, co
                                  void* stream);
 
 /* Workspace of gdn2_linear_attn_fwd (num_seqs: the packed sequence count with
- * cu_seqlens, else 0): one FP32 state per segment and head; 0 where a call runs
+ * cu_seqlens, else 0): one FP32 state per segment and head, for packed sequences two
+ * per T / (a segment's length) and head, however many sequences; 0 where a call runs
  * without one, and for invalid sizes. */
 size_t gdn2_linear_attn_fwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t num_seqs,
                                             gdn2_dtype dtype);
@@ -622,8 +623,8 @@ gdn2_status gdn2_linear_attn_bwd(const void* q, const void* k, const void* v, co
                                  int32_t zero_padding, gdn2_dtype dtype, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
-/* Workspace of gdn2_linear_attn_bwd: two FP32 states per segment and head; 0 where
- * a call runs without one, and for invalid sizes. */
+/* Workspace of gdn2_linear_attn_bwd: twice the states of the forward call's (in
+ * segments of its own); 0 where a call runs without one, and for invalid sizes. */
 size_t gdn2_linear_attn_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int32_t dk_size, int32_t dv_size,
                                             int32_t num_seqs, gdn2_dtype dtype);
 
