@@ -32,7 +32,10 @@
 // Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  P goes into its
 // product as two bf16 terms (2^-16); the copy of X that the outputs read is rounded
 // to bf16, which adds to an output, over the dk terms of its sum, what its own
-// rounding does.  X itself is FP32.  Where the caller gets it, the factor a^n z of
+// rounding does: 2.08e-3 against 64 bits in relative L2, where rounding the outputs
+// alone gives 1.66e-3.  Two terms of it reach that, at 141 us for 122 (forward) and 392
+// for 338 (backward) of the shape below, whether the wavefronts for outputs read both
+// from LDS or those for the state form X^T x from their registers.  X itself is FP32.  Where the caller gets it, the factor a^n z of
 // its update goes in as three bf16 terms that hold all 24 bits, so that it is the
 // state of FP32 arithmetic; where only the bf16 copy is read, as two.  FP32 inputs
 // are three bf16 terms throughout.
