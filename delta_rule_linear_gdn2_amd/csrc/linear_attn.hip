@@ -502,7 +502,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         Stage<T, CW, NT> z;
     };
     Staged st;
-    const int chunks = (pl.left + kC - 1) / kC;
+    const int chunks = int((uint32_t(pl.left) + kC - 1) / kC);  // left may be 2^31 - 1
     const auto length = [&](int c) { return c + 1 < chunks ? kC : pl.left - c * kC; };
     const auto first = [&](int c) { return back ? pl.tok - int64_t(c) * kC - length(c) : pl.tok + int64_t(c) * kC; };
     const auto fetch = [&](int c, Staged& g) {
