@@ -913,7 +913,8 @@ def gdn2_linear_attn_fwd(q, k, v, alpha, initial_state=None, *, output_final_sta
     in-place update).  Tokens that no packed sequence owns are not read: their
     rows are zero in a new output, and stay as they were in a given ``out``.
     ``segmented=False`` walks each sequence in one piece (no workspace);
-    ``workspace`` (uint8) is allocated when not given.
+    ``workspace`` (uint8, of at least gdn2_linear_attn_fwd_workspace_bytes of this
+    call's sizes, which smaller calls may exceed) is allocated when not given.
     """
     B, T, H, dk = _four("q", q)
     dv, dt, index = _four("v", v)[3], q.dtype, q.get_device()

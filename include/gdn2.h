@@ -574,6 +574,9 @@ size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, 
  *                   in several segments at once where there are too few of them to
  *                   fill the device, or where packed ones may differ in length.
  *                   Calls that may run at the same time need a workspace each.
+ *                   What a call needs does not grow with its size: calls that fill
+ *                   the device by themselves need none, smaller ones do.  A buffer
+ *                   for several calls is as large as the largest of their queries.
  * T may be 0 (then only final_state = initial_state is written).  H is at most
  * 2^15, B T H and num_seqs H at most 2^40.  Outputs and the workspace must not
  * overlap inputs (but final_state = initial_state) or each other.

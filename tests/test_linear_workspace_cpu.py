@@ -18,3 +18,16 @@ def test_packed_goes_by_the_segments(lib, T, H, dk, dv, dtype, least):  # noqa: 
         assert fwd % 256 == 0 and bwd % 512 == 0
     many, few = (binding.gdn2_linear_attn_fwd_workspace_bytes(1, 32768, 16, 128, 128, n, 1) for n in (5000, 7))
     assert many == few > 0
+
+
+def test_smaller_calls_may_need_more(lib):  # noqa: F811
+    """Each call's own query counts: a workspace of the larger call's size is refused where the smaller one needs more."""
+    from test_linear_cpu import BWD, FWD, call
+    from test_abi_cpu import WS
+
+    fwd, bwd = binding.gdn2_linear_attn_fwd_workspace_bytes, binding.gdn2_linear_attn_bwd_workspace_bytes
+    assert fwd(64, 4096, 4, 64, 64, 0, 1) == bwd(64, 4096, 4, 64, 64, 0, 1) == 0
+    for query, name, sizes in ((fwd, "gdn2_linear_attn_fwd", FWD), (bwd, "gdn2_linear_attn_bwd", BWD)):
+        need = query(1, 4096, 4, 64, 64, 0, 1)
+        assert need > 0
+        assert call(getattr(lib, name), list(sizes), sizes, dict(ws_bytes=need - 1)) == WS
