@@ -43,9 +43,9 @@
 // What bounds it (8 sequences x 4096 tokens x 16 heads of 128, bf16; 64 chunks a
 // workgroup, one workgroup a compute unit): 121 us, where its 537 MB take 106 at a
 // large copy's rate.  Without products the same loads, staging and stores take 112,
-// without loads the products 88.  A chunk's turn takes about 1100 cycles of matrix
-// instructions and 1100 of vector ones on each SIMD; on the two wavefronts that it
-// has they overlap in part.  Two workgroups a compute unit (128 registers a lane)
+// without loads and stores the products 84.  A chunk's turn takes about 1100 cycles of
+// matrix instructions and 1400 of vector ones on each SIMD; on the two wavefronts that
+// it has they overlap in part.  Two workgroups a compute unit (128 registers a lane)
 // spill loads in flight: 177 to 296 us; twelve wavefronts, with the state's rows halved
 // here too, take 127.  Tiles of 32 x 32 with each tile of P formed
 // twice: 143.  Loads two chunks ahead instead of one: the same.
