@@ -29,16 +29,16 @@
 // operands take the same (see Frag).  The decays of a tile are constants of the
 // head: each lane keeps its own in registers for the whole walk.
 //
-// Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  P goes into its
-// product as two bf16 terms (2^-16); the copy of X that the outputs read is rounded
-// to bf16, which adds to an output, over the dk terms of its sum, what its own
-// rounding does: 2.08e-3 against 64 bits in relative L2, where rounding the outputs
-// alone gives 1.66e-3.  Two terms of it reach that, at 141 us for 122 (forward) and 392
-// for 338 (backward) of the shape below, whether the wavefronts for outputs read both
-// from LDS or those for the state form X^T x from their registers.  X itself is FP32.  Where the caller gets it, the factor a^n z of
-// its update goes in as three bf16 terms that hold all 24 bits, so that it is the
-// state of FP32 arithmetic; where only the bf16 copy is read, as two.  FP32 inputs
-// are three bf16 terms throughout.
+// Precision.  bf16 inputs feed bf16 matrix products with FP32 sums.  What is a factor
+// again goes in as two bf16 terms (2^-16): P, the copy of X that the outputs read, and
+// the factor a^n z of X's update where the caller does not get X.  So an output is
+// rounded once, to its own type: 1.66e-3 against 64 bits in relative L2.  With one term
+// of the copy it was 2.08e-3, at 122 us instead of 139 (forward) and 340 instead of 392
+// (backward) of the shape below; the state's wavefronts forming X^T x from their
+// registers instead of the outputs' from LDS took 141.  X itself is FP32.  Where the
+// caller gets it, the factor of its update goes in as three bf16 terms that hold all
+// 24 bits, so that it is the state of FP32 arithmetic.  FP32 inputs are three bf16
+// terms throughout.
 //
 // What bounds it (8 sequences x 4096 tokens x 16 heads of 128, bf16; 64 chunks a
 // workgroup, one workgroup a compute unit): 121 us, where its 537 MB take 106 at a
@@ -375,14 +375,15 @@ struct Shape {
     static constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     static constexpr int PL = kPlanes<T>;
     static constexpr int kBytesXY = PL * kC * DA * 2, kBytesZ = PL * kC * CW * 2;
-    static constexpr int kBytesS = OUT ? PL * CW * DA * 2 : 0;
+    static constexpr int kTermsS = sizeof(T) == 2 ? 2 : 1;  // of the copy of X that outputs read, each of PL planes
+    static constexpr int kBytesS = OUT ? kTermsS * PL * CW * DA * 2 : 0;
     static constexpr int kOffY = 0, kOffZ = kBytesXY, kOffX = kOffZ + kBytesZ;
     static constexpr int kBuf = kOffX + (OUT ? kBytesXY : 0);  // one chunk's tiles
     static constexpr int kOffS = kBufs * kBuf;
     static constexpr int kOffO = kOffS + kBufs * kBytesS;      // outputs on their way to memory
     static constexpr int kBytesO = OUT ? kC * CW * int(sizeof(T)) : 0;
-    static constexpr int kOffPow = kOffO + kBufs * kBytesO;
-    static constexpr int kLds = kOffPow + 80 * 4;
+    static constexpr int kLds = kOffO + kBufs * kBytesO;
+    static_assert(kLds <= 160 * 1024, "the LDS of a compute unit");
 };
 
 // One thread's share of a chunk's tile of kC rows of D elements, in groups of eight.
@@ -483,7 +484,6 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     constexpr bool STATER = ROLE == kState;
     constexpr int NT = SH::kThreads, EB = int(sizeof(T)), TS = SH::kTiles;
     constexpr int kSteps = kC / 32, kPer = 8;   // products over a chunk's tokens, tokens a lane takes in each
-    float* const pw = reinterpret_cast<float*>(lds + SH::kOffPow);
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, l = lane & 15;
     const bool back = pl.w.back;
     const int late = back ? 1 : 0;
@@ -523,8 +523,10 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         if (OUT) g.x.store(buf + SH::kOffX, tid);
     };
     if (chunks > 0) fetch(0, st);
-    for (int i = tid; i <= kC; i += NT) pw[i] = small_power(al, i);
-    lds_barrier();  // pw
+    // The decay to the power of the lane's number, which lanes take from each other,
+    // and over a whole chunk.
+    const float mine = small_power(al, lane), whole = small_power(al, kC);
+    const auto pw = [&](int n) { return __shfl(mine, n < 0 ? 0 : n, 64); };
 
     // State wavefronts: columns 16 cb .. and rows d0 .., this lane column 16 cb + l
     // and rows d0 + 16 t + 4 g + r of tile t (d0 = 0 where OUT).
@@ -541,7 +543,8 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const int at = n - 1 + late - (32 * s + F::inner(e, g));
-                scale[s * kPer + e] = pw[at < 0 ? 0 : at];
+                const float power = pw(at);
+                scale[s * kPer + e] = at == kC ? whole : power;
             }
     };
     f32x4 X[TS];
@@ -549,11 +552,8 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
         for (int dt = 0; dt <= ROLE; ++dt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int apart = 16 * dt + l - (4 * g + r);
-                dec[dt][r] = pw[apart < 0 ? 0 : apart];
-            }
-        read = pw[16 * ROLE + l + 1 - late];
+            for (int r = 0; r < 4; ++r) dec[dt][r] = pw(16 * dt + l - (4 * g + r));
+        read = small_power(al, 16 * ROLE + l + 1 - late);
     } else {
         scales(chunks > 0 ? length(0) : kC);
         // the carry: what comes in, or the segments before this one in order
@@ -603,13 +603,44 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         }
     }
 
-    // X as the output wavefronts read it
+    // X as the output wavefronts read it: FP32 as three planes, bf16 as two, hi and lo.
+    // X - hi is a matrix product added to X, hi as the operand that two of its tiles
+    // make times minus the rows of the identity that belong to a tile (`minus`): exact,
+    // and eight matrix instructions instead of 64 vector ones (141.5 -> 139 us).
+    F minus[2];
+    if constexpr (OUT && STATER && SH::PL == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool mine = l >> 2 == g && i == 2 * h + ((l & 3) >> 1);  // row l is inner index 4 h + (l & 3) of g = l / 4
+                const uint32_t pair[1] = {mine ? (l & 1 ? 0xbf800000u : 0xbf80u) : 0u};
+                minus[h].put(i, pair);
+            }
+    }
     const auto publish = [&](unsigned char* lS) {
         if constexpr (OUT && STATER) {
-#pragma unroll
-            for (int t = 0; t < TS; ++t) {
+            const auto place = [&](int t) {
                 const int d = 16 * t + 4 * g;
-                put4_planes<SH::PL>(lS + Tile<bf16raw, DA>::off(16 * cb + l, d >> 3) + ((d & 4) << 1), CW * DA * 2, X[t]);
+                return lS + Tile<bf16raw, DA>::off(16 * cb + l, d >> 3) + ((d & 4) << 1);
+            };
+            if constexpr (SH::PL == 1) {
+                f32x4 rest[TS];
+#pragma unroll
+                for (int s = 0; s < TS / 2; ++s) {
+                    const F hi = F::from_acc(X + 2 * s);
+                    const u32x4 u = __builtin_bit_cast(u32x4, hi.x[0]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        *reinterpret_cast<uint2*>(place(2 * s + h)) = make_uint2(u[2 * h], u[2 * h + 1]);
+                        rest[2 * s + h] = minus[h].times(hi, X[2 * s + h]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < TS; ++t) put4(place(t) + CW * DA * 2, rest[t], static_cast<bf16raw*>(nullptr));
+            } else {
+#pragma unroll
+                for (int t = 0; t < TS; ++t) put4_planes<SH::PL>(place(t), CW * DA * 2, X[t]);
             }
         }
     };
@@ -623,7 +654,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         // carry (16 columns each).  Operands are read kAhead tiles before their
         // matrix instructions; left to itself the compiler reads each where it is
         // used, and the wavefront waits for LDS forty times a chunk.
-        constexpr int kTiles = NP + NC, kAhead = 8 / (ND * SH::PL), kZ = NC * NJ;
+        constexpr int kTerms = SH::kTermsS, kTiles = NP + kTerms * NC, kAhead = 8 / (ND * SH::PL), kZ = NC * NJ;
         // z's operands are read with the last of them; for FP32 rows of 128 that takes the
         // registers of loads in flight (packed FP32 backward 67.6 instead of 64.8 us).
         constexpr bool kLate = SH::PL * ND > 8;
@@ -633,13 +664,15 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
             for (int s = 0; s < ND; ++s)
                 fr[k % (kAhead + 1)][s] = k < NP ? F::template rows<DA, kC>(lY, 16 * k, s, lane)
-                                                 : F::template rows<DA, CW>(lS, 16 * (k - NP), s, lane);
+                                                 : F::template rows<DA, CW>(lS + (kTerms - 1 - (k - NP) % kTerms) * (CW * DA * 2),
+                                                                            16 * ((k - NP) / kTerms), s, lane);
         };
 #pragma unroll
         for (int s = 0; s < ND; ++s) xf[s] = F::template rows<DA, kC>(lX, 16 * ROLE, s, lane);
 #pragma unroll
         for (int k = 0; k < kAhead && k < kTiles; ++k) load(k);
         if constexpr (2 * NJ > NP) p[NP] = f32x4{0.f, 0.f, 0.f, 0.f};
+        f32x4 acc;
 #pragma unroll
         for (int k = 0; k < kTiles; ++k) {
             if (k + kAhead < kTiles) load(k + kAhead);
@@ -648,7 +681,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
                 for (int j = 0; j < kZ; ++j) zf[j] = F::template cols<CW>(lZ, 16 * (j / NJ), j % NJ, lane);
             }
             __builtin_amdgcn_sched_barrier(kMayCross);
-            f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (k < NP || (k - NP) % kTerms == 0) acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < ND; ++s) acc = fr[k % (kAhead + 1)][s].times(xf[s], acc);
             if (k < NP) {
@@ -658,14 +691,13 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
                     if (k == ROLE) acc[r] = 4 * g + r <= l ? acc[r] : 0.f;
                 }
                 p[k] = acc;
-            } else {
+            } else if ((k - NP) % kTerms == kTerms - 1) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[k - NP][r] = acc[r] * read;
+                for (int r = 0; r < 4; ++r) o[(k - NP) / kTerms][r] = acc[r] * read;
             }
         }
         // bf16: P goes in as two terms.  Rounded to one, a lone token's outputs would all
         // be off by the rounding of its q . k (3% of the forward at the training shape).
-        constexpr int kTerms = SH::PL == 1 ? 2 : 1;
         F pf[NJ][kTerms];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -743,7 +775,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     const auto update = [&](int c, const unsigned char* buf) {
         const int n = length(c);
         if (n < kC) scales(n);
-        const float over = pw[n];
+        const float over = n < kC ? pw(n) : whole;
 #pragma unroll
         for (int t = 0; t < TS; ++t)
 #pragma unroll

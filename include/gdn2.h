@@ -582,12 +582,11 @@ size_t gdn2_mixer_prologue_bwd_workspace_bytes(int32_t B, int32_t T, int32_t H, 
  * overlap inputs (but final_state = initial_state) or each other.
  *
  * bf16 inputs feed bf16 products with FP32 sums.  States that a call returns are
- * those of FP32 arithmetic.  The copy of a state that o reads is rounded to bf16,
- * which adds to o's error about as much as its own rounding does (2.1e-3 instead of
- * 1.7e-3 in relative L2); callers that need more pass FP32 tensors.  Products that are
- * factors again go in as two bf16 terms (2^-16 of them): q k^T inside a chunk and,
- * where the call returns no state, what a token adds to the state.  So o of calls with
- * and without final_state may differ in its last bits.
+ * those of FP32 arithmetic.  What is a factor again goes in as two bf16 terms (off by
+ * 2^-16, and states from 2^128 (1 - 2^-9) on count as infinite): q k^T inside a chunk,
+ * the state that o reads and, where the call returns no state, what a token adds to
+ * it.  So o is rounded once, to bf16, and o of calls with and without final_state may
+ * differ in its last bit.
  * FP32 inputs are split into three bf16 terms (products off by 2^-24; entries below
  * 1e-33 keep fewer bits, and finite ones from 2^128 (1 - 2^-9) count as infinite).
  * What is not finite in a token reaches what the recurrence lets it reach, its own and its head's
@@ -613,7 +612,7 @@ size_t gdn2_linear_attn_fwd_workspace_bytes(int32_t B, int32_t T, int32_t H, int
  *     dk_t = R_t v_t     dv_t = R_t^T k_t  d_initial_state = a R_0
  * (the last token's R adds d_final_state).  Nothing is saved by the forward
  * call.  Precision is the forward call's, with dq, dk and dv in o's place and
- * d_initial_state in final_state's (asking for it may change their last bits).  What
+ * d_initial_state in final_state's (asking for it may change their last bit).  What
  * is not finite reaches what these formulas let it reach.
  *
  *   q .. alpha, initial_state, cu_seqlens and the sizes: the forward call's.
