@@ -382,7 +382,9 @@ struct Shape {
     static constexpr int kOffS = kBufs * kBuf;
     static constexpr int kOffO = kOffS + kBufs * kBytesS;      // outputs on their way to memory
     static constexpr int kBytesO = OUT ? kC * CW * int(sizeof(T)) : 0;
-    static constexpr int kLds = kOffO + kBufs * kBytesO;
+    static constexpr bool kTable = sizeof(T) == 4;             // powers of the decay in LDS
+    static constexpr int kOffPow = kOffO + kBufs * kBytesO;
+    static constexpr int kLds = kOffPow + (kTable ? 80 * 4 : 0);
     static_assert(kLds <= 160 * 1024, "the LDS of a compute unit");
 };
 
@@ -523,10 +525,23 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         if (OUT) g.x.store(buf + SH::kOffX, tid);
     };
     if (chunks > 0) fetch(0, st);
-    // The decay to the power of the lane's number, which lanes take from each other,
-    // and over a whole chunk.
-    const float mine = small_power(al, lane), whole = small_power(al, kC);
-    const auto pw = [&](int n) { return __shfl(mine, n < 0 ? 0 : n, 64); };
+    // Powers of the decay up to a whole chunk's: a table in LDS, or, as bf16 tiles of 128
+    // x 64 leave no room for one, in each lane that of the lane's number, which the others
+    // take from it (FP32 calls take 2 to 6% longer that way).
+    float* const table = reinterpret_cast<float*>(lds + SH::kOffPow);
+    float mine = 0.f, whole = 0.f;
+    if constexpr (SH::kTable) {
+        for (int i = tid; i <= kC; i += NT) table[i] = small_power(al, i);
+        lds_barrier();
+    } else {
+        mine = small_power(al, lane), whole = small_power(al, kC);
+    }
+    const auto pw = [&](int n) {
+        n = n < 0 ? 0 : n;
+        if constexpr (SH::kTable) return table[n];
+        const float p = __shfl(mine, n & 63, 64);
+        return n == kC ? whole : p;
+    };
 
     // State wavefronts: columns 16 cb .. and rows d0 .., this lane column 16 cb + l
     // and rows d0 + 16 t + 4 g + r of tile t (d0 = 0 where OUT).
@@ -541,11 +556,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const int at = n - 1 + late - (32 * s + F::inner(e, g));
-                const float power = pw(at);
-                scale[s * kPer + e] = at == kC ? whole : power;
-            }
+            for (int e = 0; e < kPer; ++e) scale[s * kPer + e] = pw(n - 1 + late - (32 * s + F::inner(e, g)));
     };
     f32x4 X[TS];
     if constexpr (!STATER) {
@@ -553,7 +564,9 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
         for (int dt = 0; dt <= ROLE; ++dt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) dec[dt][r] = pw(16 * dt + l - (4 * g + r));
-        read = small_power(al, 16 * ROLE + l + 1 - late);
+        // each lane its own power: taken from another it costs the bf16 backward 1 to 2%
+        const int to = 16 * ROLE + l + 1 - late;
+        read = SH::kTable ? pw(to) : small_power(al, to);
     } else {
         scales(chunks > 0 ? length(0) : kC);
         // the carry: what comes in, or the segments before this one in order
@@ -775,7 +788,7 @@ __device__ __forceinline__ void walk(const LinearLaunch& a, Place pl, unsigned c
     const auto update = [&](int c, const unsigned char* buf) {
         const int n = length(c);
         if (n < kC) scales(n);
-        const float over = n < kC ? pw(n) : whole;
+        const float over = SH::kTable || n < kC ? pw(n) : whole;
 #pragma unroll
         for (int t = 0; t < TS; ++t)
 #pragma unroll
