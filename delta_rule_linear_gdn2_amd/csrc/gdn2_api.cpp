@@ -640,9 +640,9 @@ struct LinearShape {
 // as measured on MI355X for small calls: a workgroup's start and end 5, a chunk
 // 1.0 to 1.6 (bf16) or 2.4 to 4.5 (FP32) with heads up to 64 or of 128, reading a
 // segment's carry 0.5, the launch for carries 7 and half a walk's slots.  In one
-// piece / by this rule, with a state out: 4096 tokens of 16 heads of 128 forward 110 /
-// 44, 1024 tokens 32 / 21, 16384 tokens of 2 heads 418 / 59; 512 tokens stay in one
-// piece (17.1, in two 17.8).  Backward, FP32, 4096 tokens of 4 heads of 64 x 128: 494 /
+// piece / by this rule, with a state out: 4096 tokens of 16 heads of 128 forward 121 /
+// 45, 1024 tokens 35 / 22, 16384 tokens of 2 heads 459 / 55; 512 tokens stay in one
+// piece (20).  Backward, FP32, 4096 tokens of 4 heads of 64 x 128: 501 /
 // 71; counting the workgroups of its two launches as one's, 91.
 double linear_cost(int64_t groups, int64_t chunks, int64_t P, const LinearShape& sh, int64_t cus)
 {
@@ -667,13 +667,13 @@ LinearPlan linear_plan(int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, 
         // The lengths are on the device.  Segments of 0.8 of a compute unit's share of
         // the whole (sequences end inside segments, and a round of fewer chunks more is
         // better than one more chunk: FP32 backward of 3001 tokens in 7 sequences of 4
-        // heads of 64 x 128, the mean of three sets of cuts, 66 us at the whole share, 60
-        // here, 59 at 0.6), none under four chunks (FP32: two); but where the sequences
+        // heads of 64 x 128, the mean of three sets of cuts, 67 us at the whole share, 60
+        // here and at 0.6), none under four chunks (FP32: two); but where the sequences
         // alone fill the device only what is eight times their mean is cut, which cuts at
-        // random hardly ever leave (5003 tokens in 24 sequences of 6 heads 27.9 -> 27.3
-        // us, 20000 in 20 of 16 heads 152 -> 131, bf16 backward of 12000 in 6 of 8 heads
-        // 114 -> 105).  A long sequence among many short ones loses by it: 32736 tokens
-        // beside 32 of one token, 16 heads of 128, 315 us, the same without the 32 192.
+        // random hardly ever leave (5003 tokens in 24 sequences of 6 heads 30.2 -> 29.7
+        // us, 20000 in 20 of 16 heads 161 -> 144, bf16 backward of 12000 in 6 of 8 heads
+        // 125 -> 121).  A long sequence among many short ones loses by it: 32736 tokens
+        // beside 32 of one token, 16 heads of 128, 338 us, the same without the 32 210.
         const int64_t groups = int64_t(H) * sh.all_subs;
         len = int64_t(T) * groups * 4 / (5 * int64_t(cus));
         if (groups * num_seqs >= cus) len = std::max(len, 8 * int64_t(T) / num_seqs);

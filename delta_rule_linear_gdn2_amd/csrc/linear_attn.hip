@@ -33,7 +33,7 @@
 // again goes in as two bf16 terms (2^-16): P, the copy of X that the outputs read, and
 // the factor a^n z of X's update where the caller does not get X.  So an output is
 // rounded once, to its own type: 1.66e-3 against 64 bits in relative L2.  With one term
-// of the copy it was 2.08e-3, at 122 us instead of 139 (forward) and 340 instead of 392
+// of the copy it was 2.08e-3, at 125 us instead of 141 (forward) and 346 instead of 396
 // (backward) of the shape below; the state's wavefronts forming X^T x from their
 // registers instead of the outputs' from LDS took 141.  X itself is FP32.  Where the
 // caller gets it, the factor of its update goes in as three bf16 terms that hold all
@@ -41,14 +41,14 @@
 // terms throughout.
 //
 // What bounds it (8 sequences x 4096 tokens x 16 heads of 128, bf16; 64 chunks a
-// workgroup, one workgroup a compute unit): 121 us, where its 537 MB take 106 at a
+// workgroup, one workgroup a compute unit): 141 us, where its 537 MB take 106 at a
 // large copy's rate.  Without products the same loads, staging and stores take 112,
-// without loads and stores the products 84.  A chunk's turn takes about 1100 cycles of
-// matrix instructions and 1400 of vector ones on each SIMD; on the two wavefronts that
-// it has they overlap in part.  Two workgroups a compute unit (128 registers a lane)
-// spill loads in flight: 177 to 296 us; twelve wavefronts, with the state's rows halved
-// here too, take 127.  Tiles of 32 x 32 with each tile of P formed
-// twice: 143.  Loads two chunks ahead instead of one: the same.
+// without loads and stores the products 98.  A chunk's turn takes about 1500 cycles of
+// matrix instructions and 1600 of vector ones on each SIMD; on the two wavefronts that
+// it has they overlap in part.  With one term of the copy, at 122 us: two workgroups a
+// compute unit (128 registers a lane) spilled loads in flight, 177 to 296 us; twelve
+// wavefronts, with the state's rows halved here too, 127; tiles of 32 x 32 with each
+// tile of P formed twice 143; loads two chunks ahead instead of one the same.
 #include "gdn2_device.hpp"
 #include "launch.hpp"
 
